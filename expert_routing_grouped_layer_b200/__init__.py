@@ -26,12 +26,17 @@ SCORE_FN = {"sigmoid": 0, "sqrtsoftplus": 1, "softmax": 2}
 WFMT = {"bf16": 0, "fp8_e4m3_b128x128": 1, "fp4_e2m1_ue8m0_b32": 2, "mxfp4": 3, "nvfp4": 4}
 AFMT = {"bf16": 0, "fp8_e4m3_pow2_b128": 1, "mxfp8": 2, "nvfp4": 3}
 
+NORM_KIND = {"layer": 0, "rms": 1}
+DTYPE = {"bfloat16": 0, "float16": 1, "float32": 2}  # torch dtype names
+
 # symbols include/moe.h declares
 EXPORTS = ("moe_workspace_bytes", "moe_gate_topk", "moe_permute", "moe_quantize_activations",
            "moe_pack_expert_inputs", "moe_expert_gate_up", "moe_expert_down",
            "moe_grouped_swiglu", "moe_combine", "moe_layer_forward", "moe_workspace_offset",
            "moe_status_string", "moe_permute_noalloc", "moe_selftest_wait_limit",
-           "moe_rmsnorm_prologue", "moe_layer_forward_prenorm")
+           "moe_rmsnorm_prologue", "moe_layer_forward_prenorm", "moe_norm", "moe_norm_backward",
+           "moe_norm_backward_workspace_bytes", "moe_route", "moe_route_backward",
+           "moe_combine_backward")
 
 # capacity (int32 counts) of the static scratch behind moe_permute_noalloc
 MOE_PERMUTE_NOALLOC_MAX_COUNTS = 262144
@@ -69,6 +74,8 @@ _lock = threading.Lock()
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 
 
 def lib() -> ctypes.CDLL:
@@ -116,6 +123,19 @@ def lib() -> ctypes.CDLL:
                                                     _SZ, _P, _P]
             l.moe_layer_forward.restype = ctypes.c_int
             l.moe_layer_forward.argtypes = [CP, _P, _I32, WP, _P, _P, _SZ, _P, _P]
+            l.moe_norm.restype = ctypes.c_int
+            l.moe_norm.argtypes = [_I32, _I32, _P, _I64, _I32, _I32, _P, _P, _F32, _P, _I64, _P, _P, _P]
+            l.moe_norm_backward_workspace_bytes.restype = _SZ
+            l.moe_norm_backward_workspace_bytes.argtypes = [_I32, _I32]
+            l.moe_norm_backward.restype = ctypes.c_int
+            l.moe_norm_backward.argtypes = [_I32, _I32, _P, _I64, _P, _I64, _I32, _I32, _P, _P, _P,
+                                            _P, _I64, _P, _P, _P, _SZ, _P]
+            l.moe_route.restype = ctypes.c_int
+            l.moe_route.argtypes = [CP, _I32, _P, _I64, _I32, _P, _P, _P, _P]
+            l.moe_route_backward.restype = ctypes.c_int
+            l.moe_route_backward.argtypes = [CP, _I32, _P, _I64, _I32, _P, _P, _P, _I64, _P]
+            l.moe_combine_backward.restype = ctypes.c_int
+            l.moe_combine_backward.argtypes = [CP, _P, _P, _P, _P, _I32, _P, _P, _P]
             _lib = l
     return _lib
 
@@ -288,6 +308,134 @@ def moe_layer_forward_prenorm(cfg, x, T, norm_w, eps, weights, out, ws, dev_stat
                                            float(eps), ctypes.byref(w), _ptr(out), _ptr(ws),
                                            ws_bytes, _ptr(dev_status), _stream(stream)),
            "moe_layer_forward_prenorm")
+
+
+# The operators below take tensors and read sizes, strides and types from them. The
+# tensors have to lie on one CUDA device, which is current during the call; without a
+# `stream` the call goes to that device's current stream.
+def _rows(name, t, dtype=None, shape=None):
+    """(address, row stride) of a row-major matrix whose rows are dense."""
+    _tensor(name, t, dtype, shape, 2)
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s: the elements of a row must be adjacent" % name)
+    # a single row's stride is never used
+    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    if ld < t.shape[1]:
+        raise ValueError("%s: rows overlap (stride %d, %d columns)" % (name, ld, t.shape[1]))
+    return t.data_ptr(), ld
+
+
+def _vec(name, t, dtype, shape):
+    """Address of a contiguous tensor, or None for None."""
+    if t is None:
+        return None
+    _tensor(name, t, dtype, shape, len(shape))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _tensor(name, t, dtype, shape, ndim):
+    if t is None:
+        raise ValueError("%s is missing" % name)
+    if not t.is_cuda:
+        raise ValueError("%s is not on a CUDA device" % name)
+    if t.dim() != ndim or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape),
+                                                      shape if shape is not None else "%d-d" % ndim))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s is %s, not %s" % (name, t.dtype, dtype))
+
+
+def _dtype(name, t) -> int:
+    d = DTYPE.get(str(t.dtype).replace("torch.", ""))
+    if d is None:
+        raise ValueError("%s is %s: bfloat16, float16 or float32 is wanted" % (name, t.dtype))
+    return d
+
+
+def _call(fn, where, tensors, stream, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    import torch
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError("%s: tensors on %s and %s" % (where, dev, t.device))
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), where)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)), where)
+
+
+def moe_norm(x, w, b, eps, y, mean=None, rstd=None, kind="layer", stream=None):
+    """Layer norm (or RMS norm, kind="rms") of the rows of x [T, H] into y; w and b fp32
+    [H] or None; mean and rstd fp32 [T] are filled where given."""
+    import torch
+    T, H = x.shape
+    px, ldx = _rows("x", x)
+    py, ldy = _rows("y", y, x.dtype, (T, H))
+    f = torch.float32
+    _call(lib().moe_norm, "moe_norm", (x, y, w, b, mean, rstd), stream, NORM_KIND[kind],
+          _dtype("x", x), px, ldx, T, H, _vec("w", w, f, (H,)), _vec("b", b, f, (H,)), float(eps), py,
+          ldy, _vec("mean", mean, f, (T,)), _vec("rstd", rstd, f, (T,)))
+
+
+def moe_norm_backward_workspace_bytes(T: int, H: int) -> int:
+    return lib().moe_norm_backward_workspace_bytes(int(T), int(H))
+
+
+def moe_norm_backward(dy, x, w, mean, rstd, dx, dw, db, ws, kind="layer", stream=None):
+    """Gradients of moe_norm: dx [T, H] like x, dw and db fp32 [H]; each may be None. ws: at
+    least moe_norm_backward_workspace_bytes(T, H) bytes (None without dw and db)."""
+    import torch
+    T, H = x.shape
+    px, ldx = _rows("x", x)
+    pg, ldg = _rows("dy", dy, x.dtype, (T, H))
+    pd, ldd = _rows("dx", dx, x.dtype, (T, H)) if dx is not None else (None, H)
+    f = torch.float32
+    _call(lib().moe_norm_backward, "moe_norm_backward", (x, dy, w, mean, rstd, dx, dw, db, ws), stream,
+          NORM_KIND[kind], _dtype("x", x), pg, ldg, px, ldx, T, H, _vec("w", w, f, (H,)),
+          _vec("mean", mean, f, (T,)), _vec("rstd", rstd, f, (T,)), pd, ldd, _vec("dw", dw, f, (H,)),
+          _vec("db", db, f, (H,)), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+
+
+def moe_route(cfg, logits, bias, topk_idx, topk_w, stream=None):
+    """Experts and weights from router logits [T, E] (bf16, f16 or fp32) and a balance bias
+    fp32 [E] or None: topk_idx int32 [T, k], topk_w fp32 [T, k]."""
+    import torch
+    c = _cfg(cfg)
+    T, k, E = logits.shape[0], c.num_experts_per_tok, c.n_routed_experts
+    p, ld = _rows("logits", logits, None, (T, E))
+    _call(lib().moe_route, "moe_route", (logits, bias, topk_idx, topk_w), stream, ctypes.byref(c),
+          _dtype("logits", logits), p, ld, T, _vec("bias", bias, torch.float32, (E,)),
+          _vec("topk_idx", topk_idx, torch.int32, (T, k)), _vec("topk_w", topk_w, torch.float32, (T, k)))
+
+
+def moe_route_backward(cfg, logits, topk_idx, dtopk_w, dlogits, stream=None):
+    """dlogits [T, E], like logits, from the gradient dtopk_w fp32 [T, k] of moe_route's weights."""
+    import torch
+    c = _cfg(cfg)
+    T, k, E = logits.shape[0], c.num_experts_per_tok, c.n_routed_experts
+    p, ld = _rows("logits", logits, None, (T, E))
+    pd, ldd = _rows("dlogits", dlogits, logits.dtype, (T, E))
+    _call(lib().moe_route_backward, "moe_route_backward", (logits, topk_idx, dtopk_w, dlogits), stream,
+          ctypes.byref(c), _dtype("logits", logits), p, ld, T,
+          _vec("topk_idx", topk_idx, torch.int32, (T, k)),
+          _vec("dtopk_w", dtopk_w, torch.float32, (T, k)), pd, ldd)
+
+
+def moe_combine_backward(cfg, dout, y, row_of, topk_w, dy, dtopk_w, stream=None):
+    """Gradients of moe_combine: dy bf16 [N, H] (rows of dropped pairs stay as they are) and
+    dtopk_w fp32 [T, k] (None: not wanted, y may then be None)."""
+    import torch
+    c = _cfg(cfg)
+    T, k, H = dout.shape[0], c.num_experts_per_tok, c.hidden
+    bf, f = torch.bfloat16, torch.float32
+    _call(lib().moe_combine_backward, "moe_combine_backward", (dout, y, row_of, topk_w, dy, dtopk_w),
+          stream, ctypes.byref(c), _vec("dout", dout, bf, (T, H)), _vec("y", y, bf, (T * k, H)),
+          _vec("row_of", row_of, torch.int32, (T * k,)), _vec("topk_w", topk_w, f, (T, k)), T,
+          _vec("dy", dy, bf, (T * k, H)), _vec("dtopk_w", dtopk_w, f, (T, k)))
 
 
 class MoELayer:

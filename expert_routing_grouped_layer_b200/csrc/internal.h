@@ -107,6 +107,24 @@ cudaError_t launch_combine(const void* y, const void* shared_y, int S, const int
 // sets MOE_DEV_TIMEOUT in *status
 cudaError_t launch_wait_limit_selftest(int32_t* status, cudaStream_t st);
 
+// Row norms (norm.cu), routing of given logits (route.cu), the combine's gradient
+// (combine_bwd.cu); dtype MOE_T_*, ld* in elements.
+cudaError_t launch_norm_fwd(int kind, int dtype, const void* x, long ldx, int T, int H, const float* w,
+                            const float* b, float eps, void* y, long ldy, float* mean, float* rstd,
+                            cudaStream_t st);
+size_t norm_backward_ws(int T, int H);
+cudaError_t launch_norm_bwd(int kind, int dtype, const void* dy, long lddy, const void* x, long ldx,
+                            int T, int H, const float* w, const float* mean, const float* rstd,
+                            void* dx, long lddx, float* dw, float* db, float* part, cudaStream_t st);
+cudaError_t launch_route(const moe_config* c, int dtype, const void* logits, long ld, int T,
+                         const float* bias, int32_t* idx, float* w, cudaStream_t st);
+cudaError_t launch_route_backward(const moe_config* c, int dtype, const void* logits, long ld, int T,
+                                  const int32_t* idx, const float* dw, void* dl, long ldd,
+                                  cudaStream_t st);
+cudaError_t launch_combine_backward(const void* dout, const void* y, const int32_t* row_of,
+                                    const float* w, int T, int k, int H, void* dy, float* dw,
+                                    cudaStream_t st);
+
 struct GroupedGemmArgs {
     // problem
     int gemm;           // 1: gate/up + SwiGLU, 2: down projection

@@ -1,0 +1,589 @@
+// route.cu -- expert selection from given router logits, forward and backward.
+//
+// "DeepSeek V3架构拆解：Kimi-K2-Thinking-NVFP4的MLA注意力与MoE路由实现原理", 三.1-三.3: s = score(l)
+// (sigmoid; sqrt(softplus), "DeepSeek-V4-Pro 架构与代码概述" 架构; softmax over the row),
+// s' = s + bias, the topk_group best of n_group groups by the sum of their two largest
+// s', the k largest s' of those, weights s (divided by their sum) times the routed
+// scaling factor. An expert with a logit or bias of -inf is masked: never chosen.
+//
+// Which expert is chosen is decided exactly. Without bias and groups the order of s' is
+// the order of the logits. Otherwise s' is computed in fp32 with a known error bound;
+// where two values that the outcome depends on lie closer than twice the bound, they
+// are computed in double precision and compared there (then the larger logit, then the
+// lower index). That happens for about one token in a thousand, so the fp32 path sets
+// the speed.
+//
+// One warp per token holds the row in registers. The cost is the exponentials and the
+// k rounds of a warp-wide maximum (redux.sync on order-preserving integer keys), not
+// the bytes.
+#include <climits>
+#include <cmath>
+
+#include "internal.h"
+#include "sm100.cuh"
+#include "types.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr float kInf = INFINITY;
+
+struct RouteParams {
+    const void* logits;
+    const float* bias;
+    int32_t* idx;
+    float* w;
+    long ld;
+    int T, E, k, n_group, topk_group, norm, score_fn;
+    float rsf;
+};
+
+// fp32 keys ordered as unsigned integers (finite values and infinities).
+__device__ __forceinline__ uint32_t key_of(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+__device__ __forceinline__ float warp_max(float v) { return value_of(__reduce_max_sync(kFull, key_of(v))); }
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+// Scores. m and z: the row's largest logit and sum of exponentials (softmax).
+__device__ __forceinline__ float score_f(float l, int fn, float m, float inv_z) {
+    if (fn == MOE_SCORE_SIGMOID) return __fdividef(1.0f, 1.0f + expf(-l));
+    if (fn == MOE_SCORE_SQRTSOFTPLUS) return sqrtf(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
+    return expf(l - m) * inv_z;
+}
+__device__ __forceinline__ double score_d(double l, int fn, double m, double z) {
+    if (fn == MOE_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-l));
+    if (fn == MOE_SCORE_SQRTSOFTPLUS) return sqrt(fmax(l, 0.0) + log1p(exp(-fabs(l))));
+    return exp(l - m) / z;
+}
+
+// The row as the slow paths see it: masked elements are -inf.
+template <typename T>
+struct Row {
+    const T* l;
+    const float* bias;
+    int E, gsz, fn;
+    float m;
+    double z;
+    uint32_t kept;  // bit g: group g is kept
+    __device__ __forceinline__ float logit(int e) const { return to_f32<T>(l[e]) + 0.0f; }
+    __device__ __forceinline__ double sel(int e, float le) const {
+        const float b = bias ? bias[e] : 0.f;
+        if (le == -kInf || b == -kInf) return -(double)kInf;
+        return score_d((double)le, fn, (double)m, z) + (double)b;
+    }
+};
+
+template <typename T>
+__device__ __noinline__ double row_z(const T* l, int E, float m) {
+    double z = 0.0;
+    for (int e = threadIdx.x & 31; e < E; e += 32) {
+        const float le = to_f32<T>(l[e]);
+        if (le != -kInf) z += exp((double)le - (double)m);
+    }
+    return warp_sum(z);
+}
+
+// The kept groups by their scores in double precision.
+template <typename T>
+__device__ __noinline__ uint32_t groups_exact(Row<T> r, int n_group, int topk_group) {
+    const int lane = threadIdx.x & 31;
+    double gs = -(double)kInf;
+    for (int g = 0; g < n_group; ++g) {
+        double b1 = -(double)kInf, b2 = b1;
+        for (int e = g * r.gsz + lane; e < (g + 1) * r.gsz; e += 32) {
+            const double v = r.sel(e, r.logit(e));
+            if (v > b1) { b2 = b1; b1 = v; }
+            else if (v > b2) b2 = v;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const double o1 = __shfl_xor_sync(kFull, b1, o), o2 = __shfl_xor_sync(kFull, b2, o);
+            b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+            b1 = fmax(b1, o1);
+        }
+        if (lane == g) gs = b2 == -(double)kInf ? b1 : b1 + b2;
+    }
+    int rank = 0;
+    for (int g = 0; g < n_group; ++g) {
+        const double o = __shfl_sync(kFull, gs, g);
+        rank += (o > gs || (o == gs && g < lane)) ? 1 : 0;
+    }
+    return __ballot_sync(kFull, lane < n_group && rank < topk_group);
+}
+
+__device__ __forceinline__ bool better_d(double va, float la, int ia, double vb, float lb, int ib) {
+    return va > vb || (va == vb && (la > lb || (la == lb && ia < ib)));
+}
+
+// Orders up to 32 candidates (one per lane, e < 0: none) by their exact values; the
+// expert of rank r lands in lane r (-1 where there is none).
+template <typename T>
+__device__ __noinline__ int rank_exact(Row<T> r, int e, int count) {
+    const int lane = threadIdx.x & 31;
+    const float l = e >= 0 ? r.logit(e) : 0.f;
+    const double v = e >= 0 ? r.sel(e, l) : -(double)kInf;
+    int rank = 0;
+    for (int c = 0; c < count; ++c) {
+        const double vo = __shfl_sync(kFull, v, c);
+        const float lo = __shfl_sync(kFull, l, c);
+        const int eo = __shfl_sync(kFull, e, c);
+        rank += better_d(vo, lo, eo, v, l, e) ? 1 : 0;
+    }
+    if (e < 0) rank = 64;
+    int mine = -1;
+    for (int c = 0; c < count; ++c) {
+        const int at = __shfl_sync(kFull, rank, c), eo = __shfl_sync(kFull, e, c);
+        if (at == lane) mine = eo;
+    }
+    return mine;
+}
+
+// More than 32 candidates lie within the error bound (rows of nearly equal scores):
+// k rounds, each a maximum of the exact values over the experts not yet chosen.
+template <typename T>
+__device__ __noinline__ int topk_exact(Row<T> r, int k) {
+    const int lane = threadIdx.x & 31;
+    uint32_t taken = 0;  // bit i: expert lane + 32 i
+    int mine = -1;
+    for (int round = 0; round < k; ++round) {
+        double bv = -(double)kInf;
+        float bl = -kInf;
+        int be = INT_MAX;
+        for (int e = lane, i = 0; e < r.E; e += 32, ++i) {
+            if (((taken >> i) & 1u) || !((r.kept >> (e / r.gsz)) & 1u)) continue;
+            const float l = r.logit(e);
+            const double v = r.sel(e, l);
+            if (v != -(double)kInf && better_d(v, l, e, bv, bl, be)) { bv = v; bl = l; be = e; }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const double ov = __shfl_xor_sync(kFull, bv, o);
+            const float ol = __shfl_xor_sync(kFull, bl, o);
+            const int oe = __shfl_xor_sync(kFull, be, o);
+            if (better_d(ov, ol, oe, bv, bl, be)) { bv = ov; bl = ol; be = oe; }
+        }
+        if (be == INT_MAX) break;
+        if ((be & 31) == lane) taken |= 1u << (be >> 5);
+        if (round == lane) mine = be;
+    }
+    return mine;
+}
+
+// Lane j's share s_j / sum s of the chosen scores (j < k, valid), and, without
+// normalisation, s_j itself. Scores far below the fp32 range (every chosen logit
+// around -90 and less) are taken in double precision.
+__device__ __forceinline__ float chosen_weight(float l, bool valid, int fn, int norm, float m, float z) {
+    float s = valid ? score_f(l, fn, m, 1.0f / z) : 0.f;
+    if (!norm) return s;
+    if (__any_sync(kFull, valid && s < 1e-30f)) {
+        const double sd = valid ? score_d((double)l, fn, (double)m, (double)z) : 0.0;
+        const double sum = warp_sum(sd);
+        return sum > 0.0 ? (float)(sd / sum) : 0.f;
+    }
+    const float sum = warp_sum(s);
+    return sum > 0.f ? s / sum : 0.f;
+}
+
+// Lane (g, sub) of L lanes per group holds the group's elements (sub + L i) VEC + v:
+// a group's two largest come from the lanes of that group alone, and without groups
+// (L = 32) a load instruction covers consecutive elements.
+template <typename T, int VEC, int NI>
+__global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
+    pdl_wait();
+    pdl_trigger();
+    constexpr int J = NI * VEC;
+    typedef unsigned long long u64;
+    __shared__ int list[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long t = (long)blockIdx.x * (blockDim.x >> 5) + warp;
+    if (t >= p.T) return;
+    const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+    const int gsz = p.E / p.n_group;
+    const int g = lane / L, sub = lane - g * L;
+    const int nvec = g < p.n_group ? gsz / VEC : 0;
+    const int e0 = g * gsz + sub * VEC;  // element (i, v) is e0 + i L VEC + v
+
+    Pack<T, VEC> raw[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+        if (sub + i * L < nvec) raw[i] = reinterpret_cast<const Pack<T, VEC>*>(row + e0)[i * L];
+    const bool by_logit = !p.bias && p.n_group == 1;
+    float sel[J];
+    bool bad = false;
+    float lm = -kInf;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            float l = sub + i * L < nvec ? to_f32<T>(raw[i].v[v]) + 0.0f : -kInf;
+            bad |= !(l < kInf);
+            lm = fmaxf(lm, l);
+            sel[i * VEC + v] = l;
+        }
+    }
+    // the row's maximum and sum of exponentials (softmax), or the largest score's bound
+    float m = 0.f, z = 1.f, scale = 1.f;
+    if (p.score_fn != MOE_SCORE_SIGMOID) {
+        const float top = warp_max(bad ? -kInf : lm);
+        if (p.score_fn == MOE_SCORE_SOFTMAX) {
+            m = top == -kInf ? 0.f : top;
+            float zs = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) zs += expf(sel[j] - m);
+            z = warp_sum(zs);
+        } else {
+            scale = fmaxf(1.f, sqrtf(fmaxf(top, 0.f) + 1.f));
+        }
+    }
+    if (!by_logit) {
+        const float inv_z = 1.0f / z;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const int j = i * VEC + v;
+                const float b = p.bias && sub + i * L < nvec ? p.bias[e0 + i * L * VEC + v] : 0.f;
+                bad |= !(b < kInf);
+                sel[j] = sel[j] == -kInf || b == -kInf ? -kInf : score_f(sel[j], p.score_fn, m, inv_z) + b;
+            }
+        }
+    }
+    if (__any_sync(kFull, bad)) {  // a NaN or +inf among the row's logits or the biases
+        if (lane < p.k) {
+            p.idx[t * p.k + lane] = -1;
+            p.w[t * p.k + lane] = NAN;
+        }
+        return;
+    }
+    // |computed s' - s'| <= eps * max(scale, |s'|): a few units of 2^-24 for the sigmoid and
+    // sqrt-softplus, up to J + 5 more for the softmax's sum
+    const float eps = p.score_fn == MOE_SCORE_SOFTMAX ? 7.7e-6f : 4.8e-7f;
+
+    uint32_t kept = kFull;
+    if (p.n_group > 1) {
+        float b1 = -kInf, b2 = -kInf;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            b2 = fmaxf(b2, fminf(b1, sel[j]));
+            b1 = fmaxf(b1, sel[j]);
+        }
+        for (int o = L >> 1; o > 0; o >>= 1) {
+            const float o1 = __shfl_xor_sync(kFull, b1, o), o2 = __shfl_xor_sync(kFull, b2, o);
+            b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+            b1 = fmaxf(b1, o1);
+        }
+        const float gs = b2 == -kInf ? b1 : b1 + b2;
+        int rank = 0;
+        for (int h = 0; h < p.n_group; ++h) {
+            const float o = __shfl_sync(kFull, gs, h * L);
+            rank += (o > gs || (o == gs && h < g)) ? 1 : 0;
+        }
+        const bool real = g < p.n_group, keep = real && rank < p.topk_group;
+        const float lo = -warp_max(keep ? -gs : -kInf);          // smallest kept
+        const float hi = warp_max(real && !keep ? gs : -kInf);   // largest left out
+        const float mag = warp_max(real && b1 != -kInf ? fmaxf(fabsf(b1), b2 == -kInf ? 0.f : fabsf(b2)) : 0.f);
+        const float tol = 5.f * eps * fmaxf(scale, mag);  // two sums of two values each
+        if (hi != -kInf && !(lo - hi > tol)) {
+            const double zd = p.score_fn == MOE_SCORE_SOFTMAX ? row_z<T>(row, p.E, m) : 1.0;
+            kept = groups_exact<T>(Row<T>{row, p.bias, p.E, gsz, p.score_fn, m, zd, kFull}, p.n_group,
+                                   p.topk_group);
+        } else {
+            kept = 0;
+            for (int h = 0; h < p.n_group; ++h)
+                kept |= (__shfl_sync(kFull, (int)keep, h * L) & 1) << h;
+        }
+        if (!((kept >> (g < p.n_group ? g : 0)) & 1u)) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) sel[j] = -kInf;
+        }
+    }
+
+    // Each lane caches its two best elements; a round is one warp maximum over the
+    // lanes' heads. The winner pops its head and rescans when its cache is empty.
+    u64 avail = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        if (sel[j] != -kInf) avail |= 1ull << j;
+    uint32_t k1, k2;
+    int j1, j2;
+    auto refill = [&]() {
+        k1 = k2 = 0u;
+        j1 = j2 = -1;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const uint32_t kk = (avail >> j) & 1ull ? key_of(sel[j]) : 0u;
+            if (kk > k1) {
+                k2 = k1; j2 = j1;
+                k1 = kk; j1 = j;
+            } else if (kk > k2) {
+                k2 = kk; j2 = j;
+            }
+        }
+    };
+    // within a lane the element index grows with j, so the first of equal keys is the lower
+    auto expert = [&](int j) { return e0 + (j / VEC) * L * VEC + j % VEC; };
+    refill();
+    int my_e = -1;
+    uint32_t my_key = 0u, last = 0u;
+    for (int r = 0; r < p.k; ++r) {
+        const uint32_t top = __reduce_max_sync(kFull, k1);
+        if (top == 0u) break;  // fewer than k experts are left
+        const uint32_t who = __ballot_sync(kFull, k1 == top);
+        int win = __ffs(who) - 1;
+        if (who & (who - 1)) {  // equal keys in several lanes: the lowest index
+            const int low = __reduce_min_sync(kFull, k1 == top ? expert(j1) : INT_MAX);
+            win = __ffs(__ballot_sync(kFull, k1 == top && expert(j1) == low)) - 1;
+        }
+        const int e = __shfl_sync(kFull, j1 >= 0 ? expert(j1) : -1, win);
+        if (lane == r) {
+            my_e = e;
+            my_key = top;
+        }
+        last = top;
+        if (lane == win) {
+            avail &= ~(1ull << j1);
+            k1 = k2; j1 = j2;
+            k2 = 0u; j2 = -1;
+            if (k1 == 0u && avail) refill();
+        }
+    }
+    const float my_l0 = my_e >= 0 ? to_f32<T>(row[my_e]) + 0.0f : 0.f;
+    float my_l = my_l0;
+    if (!by_logit && last != 0u) {
+        // values that the bound cannot tell apart and that are not the same number: among
+        // the chosen one after the other, and of those left out against the last chosen
+        const float mine = value_of(my_key);
+        const float my_b = my_e >= 0 && p.bias ? p.bias[my_e] : 0.f;
+        const uint32_t next_key = __shfl_down_sync(kFull, my_key, 1);
+        const float next_l = __shfl_down_sync(kFull, my_l0, 1), next_b = __shfl_down_sync(kFull, my_b, 1);
+        const float tol = 2.f * eps * fmaxf(scale, fabsf(mine));
+        bool near = lane + 1 < p.k && next_key != 0u && mine - value_of(next_key) <= tol &&
+                    !(next_l == my_l0 && next_b == my_b);
+        const int chosen = __popc(__ballot_sync(kFull, my_e >= 0));
+        const float last_v = value_of(last);
+        const float cut = last_v - 2.f * eps * fmaxf(scale, fabsf(last_v));
+        const float ll = __shfl_sync(kFull, my_l0, chosen - 1), lb = __shfl_sync(kFull, my_b, chosen - 1);
+        if (k1 != 0u && value_of(k1) >= cut) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (((avail >> j) & 1ull) && sel[j] >= cut) {
+                    const int e = expert(j);
+                    near |= !(to_f32<T>(row[e]) + 0.0f == ll && (p.bias ? p.bias[e] : 0.f) == lb);
+                }
+        }
+        if (__any_sync(kFull, near)) {
+            // candidates: everything chosen or not below the cut
+            int count = 0;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const bool in = sel[j] >= cut;
+                const uint32_t who = __ballot_sync(kFull, in);
+                const int at = count + __popc(who & ((1u << lane) - 1));
+                if (in && at < 32) list[warp][at] = expert(j);
+                count += __popc(who);
+            }
+            __syncwarp();
+            const double zd = p.score_fn == MOE_SCORE_SOFTMAX ? row_z<T>(row, p.E, m) : 1.0;
+            const Row<T> r{row, p.bias, p.E, gsz, p.score_fn, m, zd, p.n_group > 1 ? kept : kFull};
+            if (count <= 32) {
+                my_e = rank_exact<T>(r, lane < count ? list[warp][lane] : -1, count);
+                if (lane >= p.k) my_e = -1;
+            } else {
+                my_e = topk_exact<T>(r, p.k);
+            }
+            my_l = my_e >= 0 ? to_f32<T>(row[my_e]) + 0.0f : 0.f;
+        }
+    }
+    const float w = chosen_weight(my_l, my_e >= 0, p.score_fn, p.norm, m, z);
+    if (lane < p.k) {
+        p.idx[t * p.k + lane] = my_e;
+        p.w[t * p.k + lane] = w * p.rsf;
+    }
+}
+
+struct RouteBwd {
+    const void* logits;
+    const int32_t* idx;
+    const float* dw;
+    void* dl;
+    long ld, ldd;
+    int T, E, k, norm, score_fn;
+    float rsf;
+};
+
+// d s_j / d l_j over s_j: sigmoid 1 - s, sqrt-softplus sig(l) / (2 softplus(l)) (1/2 far below
+// zero, where both go to exp(l)).
+__device__ __forceinline__ float log_slope(float l, int fn) {
+    if (fn == MOE_SCORE_SIGMOID) return 1.0f / (1.0f + expf(l));
+    const float e = expf(-fabsf(l));
+    const float sp = fmaxf(l, 0.0f) + log1pf(e);
+    if (l < -40.0f) return 0.5f;
+    return (l >= 0.0f ? 1.0f : e) / (1.0f + e) * 0.5f / sp;
+}
+
+// One warp per token: lane j works out slot j's gradient, the warp writes the row. Only a
+// softmax without renormalisation gives the other experts a gradient (-s_e <g s>) and
+// reads the whole row; every other row is zeros and the k values.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwd p) {
+    pdl_wait();
+    pdl_trigger();
+    constexpr int NI = 32 / VEC;
+    const int lane = threadIdx.x & 31;
+    const long t = (long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (t >= p.T) return;
+    const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+    T* out = static_cast<T*>(p.dl) + t * p.ldd;
+    const int nvec = p.E / VEC;
+    const bool dense = p.score_fn == MOE_SCORE_SOFTMAX && !p.norm;
+
+    int e = lane < p.k ? p.idx[t * p.k + lane] : -1;
+    if (e < 0 || e >= p.E) e = -1;
+    const bool valid = e >= 0;
+    const float l = valid ? to_f32<T>(row[e]) : 0.f;
+    const float g = valid ? p.dw[t * p.k + lane] * p.rsf : 0.f;
+    const bool any = __any_sync(kFull, valid);
+
+    float s[NI * VEC];
+    float m = 0.f, z = 1.f;
+    if (p.score_fn == MOE_SCORE_SOFTMAX) {
+        if (dense && any) {
+            float top = -kInf;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                Pack<T, VEC> raw;
+                if (lane + 32 * i < nvec) raw = reinterpret_cast<const Pack<T, VEC>*>(row)[lane + 32 * i];
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    s[i * VEC + v] = lane + 32 * i < nvec ? to_f32<T>(raw.v[v]) : -kInf;
+                    top = fmaxf(top, s[i * VEC + v]);
+                }
+            }
+            m = warp_max(top);
+            float zs = 0.f;
+#pragma unroll
+            for (int j = 0; j < NI * VEC; ++j) {
+                s[j] = expf(s[j] - m);
+                zs += s[j];
+            }
+            z = warp_sum(zs);
+        } else {
+            m = warp_max(valid ? l : -kInf);  // renormalised: a softmax over the chosen
+        }
+    }
+    const float w = chosen_weight(l, valid, p.score_fn, p.norm, m, z);
+    const float dot = p.norm || dense ? warp_sum(g * w) : 0.f;
+    float d = p.norm ? w * (g - dot) : w * g;
+    if (p.score_fn != MOE_SCORE_SOFTMAX) d *= log_slope(l, p.score_fn);
+    // an expert in several slots gets the slots' sum, added in slot order
+    const uint32_t same = __match_any_sync(kFull, valid ? e : -1 - lane);
+    if (__any_sync(kFull, valid && (same & (same - 1)))) {
+        float sum = 0.f;
+        for (int c = 0; c < p.k; ++c) {
+            const float o = __shfl_sync(kFull, d, c);
+            if ((same >> c) & 1u) sum += o;
+        }
+        d = sum;
+    }
+    if (dense) d -= w * dot;
+
+    const float back = dense && any ? -dot / z : 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        if (lane + 32 * i >= nvec) continue;
+        Pack<T, VEC> o;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) o.v[v] = from_f32<T>(dense && any ? s[i * VEC + v] * back : 0.f);
+        reinterpret_cast<Pack<T, VEC>*>(out)[lane + 32 * i] = o;
+    }
+    __syncwarp();
+    if (valid) out[e] = from_f32<T>(d);
+}
+
+template <typename T, int VEC, int NI>
+void fwd(const RouteParams& p, int L, cudaStream_t st) {
+    // a few warps per CTA for small batches, so that they spread over the SMs
+    const int warps = p.T >= 16 * num_sms() ? 8 : 2;
+    launch_pdl(route_fwd_kernel<T, VEC, NI>, (p.T + warps - 1) / warps, warps * 32, 0, st, p, L);
+}
+
+template <typename T>
+void fwd_type(const RouteParams& p, bool vec, cudaStream_t st) {
+    constexpr int V = kFullVec<T>;
+    int L = 32;
+    while (L * p.n_group > 32) L >>= 1;
+    const int gsz = p.E / p.n_group;
+    if (vec) {
+        const int ni = (gsz / V + L - 1) / L;
+        if (ni <= 1) return fwd<T, V, 1>(p, L, st);
+        if (ni <= 2) return fwd<T, V, 2>(p, L, st);
+        if (V == 4 && ni <= 3) return fwd<T, V, 3>(p, L, st);
+        if (ni <= 4) return fwd<T, V, 4>(p, L, st);
+        if (ni <= 8) return fwd<T, V, 8>(p, L, st);
+        if (V == 4) return fwd<T, V, 64 / V>(p, L, st);
+    }
+    const int ni = (gsz + L - 1) / L;
+    if (ni <= 4) fwd<T, 1, 4>(p, L, st);
+    else if (ni <= 16) fwd<T, 1, 16>(p, L, st);
+    else if (ni <= 32) fwd<T, 1, 32>(p, L, st);
+    else fwd<T, 1, 64>(p, L, st);
+}
+
+inline bool rows16(const void* p, long ld, int es) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * es) % 16 == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_route(const moe_config* c, int dtype, const void* logits, long ld, int T,
+                         const float* bias, int32_t* idx, float* w, cudaStream_t st) {
+    const RouteParams p{logits, bias, idx, w, ld, T, c->n_routed_experts, c->num_experts_per_tok,
+                        c->n_group, c->topk_group, c->norm_topk_prob, c->score_fn,
+                        c->routed_scaling_factor};
+    const int es = esize(dtype);
+    const bool vec = (p.E / p.n_group) % (16 / es) == 0 && rows16(logits, ld, es);
+    if (dtype == MOE_T_BF16) fwd_type<__nv_bfloat16>(p, vec, st);
+    else if (dtype == MOE_T_F16) fwd_type<__half>(p, vec, st);
+    else fwd_type<float>(p, vec, st);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_route_backward(const moe_config* c, int dtype, const void* logits, long ld, int T,
+                                  const int32_t* idx, const float* dw, void* dl, long ldd,
+                                  cudaStream_t st) {
+    const RouteBwd p{logits, idx, dw, dl, ld, ldd, T, c->n_routed_experts, c->num_experts_per_tok,
+                     c->norm_topk_prob, c->score_fn, c->routed_scaling_factor};
+    const int es = esize(dtype);
+    const bool vec = p.E % (16 / es) == 0 && rows16(logits, ld, es) && rows16(dl, ldd, es);
+    const unsigned grid = (unsigned)((T + 7) / 8);
+    if (dtype == MOE_T_BF16) {
+        if (vec) launch_pdl(route_bwd_kernel<__nv_bfloat16, 8>, grid, 256, 0, st, p);
+        else launch_pdl(route_bwd_kernel<__nv_bfloat16, 1>, grid, 256, 0, st, p);
+    } else if (dtype == MOE_T_F16) {
+        if (vec) launch_pdl(route_bwd_kernel<__half, 8>, grid, 256, 0, st, p);
+        else launch_pdl(route_bwd_kernel<__half, 1>, grid, 256, 0, st, p);
+    } else {
+        if (vec) launch_pdl(route_bwd_kernel<float, 4>, grid, 256, 0, st, p);
+        else launch_pdl(route_bwd_kernel<float, 1>, grid, 256, 0, st, p);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -116,6 +116,15 @@ typedef enum {
  * the bf16 input. */
 #define MOE_A_NVFP4 3
 
+/* element types of the row operators below (moe_norm, moe_route, moe_linear) */
+#define MOE_T_BF16 0
+#define MOE_T_F16 1
+#define MOE_T_F32 2
+
+/* norm kinds */
+#define MOE_NORM_LAYER 0
+#define MOE_NORM_RMS 1
+
 /* Layer configuration; field names follow the configuration the pages quote. */
 typedef struct {
     int32_t hidden;                   /* H, multiple of 128                     */
@@ -321,6 +330,82 @@ moe_status moe_layer_forward_prenorm(const moe_config *cfg, const void *x, int32
                                      const float *norm_w, float eps, const moe_weights *w,
                                      void *out, void *ws, size_t ws_bytes, int32_t *dev_status,
                                      void *stream);
+
+/* Row norms for training and for activations of any type ([V3] 三, the decoder
+ * layer's norms; moe_rmsnorm_prologue is the serving form that also quantises).
+ *  kind MOE_NORM_LAYER: y = (x - mean) * rstd * w + b with mean = sum_h x_h / H and
+ *       rstd = 1 / sqrt(sum_h (x_h - mean)^2 / H + eps);
+ *  kind MOE_NORM_RMS: the same with mean = 0.
+ *  x, y: rows of `dtype` (MOE_T_*), [T][H] with row strides ldx, ldy in elements
+ *  (>= H); y may be x when the strides are equal. w, b: fp32 [H], each may be NULL
+ *  (ones, zeros). mean, rstd: fp32 [T], written for the backward pass, each may be
+ *  NULL; mean is not written for MOE_NORM_RMS. eps finite, >= 0. 1 <= H <= 16384,
+ *  larger rows return MOE_ERR_UNSUPPORTED. Statistics and arithmetic are fp32, y is
+ *  rounded once. Rows whose base, stride and length are multiples of 16 bytes move
+ *  by 16-byte accesses; others element by element. */
+moe_status moe_norm(int32_t kind, int32_t dtype, const void *x, int64_t ldx, int32_t T, int32_t H,
+                    const float *w, const float *b, float eps, void *y, int64_t ldy, float *mean,
+                    float *rstd, void *stream);
+
+/* Gradient of moe_norm. With n = (x - mean) * rstd and g = w * dy:
+ *  dx = rstd * (g - sum(g)/H - n * sum(g n)/H)   (MOE_NORM_RMS: without sum(g)/H),
+ *  dw = sum_t dy n, db = sum_t dy.
+ *  dy, x, dx: rows of `dtype`; mean (MOE_NORM_LAYER only) and rstd as moe_norm wrote
+ *  them; w NULL = ones. dx, dw, db may each be NULL (not wanted); db is not written
+ *  for MOE_NORM_RMS. dx may be dy or x when the strides are equal. dw and db fp32
+ *  [H] are overwritten (zeros for T = 0); their sums run in a fixed order, so equal
+ *  calls on one kind of GPU give equal bits. ws: moe_norm_backward_workspace_bytes
+ *  bytes, 16-byte aligned (unused, may be NULL, when dw and db are NULL). */
+moe_status moe_norm_backward(int32_t kind, int32_t dtype, const void *dy, int64_t lddy,
+                             const void *x, int64_t ldx, int32_t T, int32_t H, const float *w,
+                             const float *mean, const float *rstd, void *dx, int64_t lddx,
+                             float *dw, float *db, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace of moe_norm_backward on the current device; 0 for invalid sizes. */
+size_t moe_norm_backward_workspace_bytes(int32_t T, int32_t H);
+
+/* Expert selection from router logits the caller computed ([V3] 三.1-三.3; the rules
+ * of moe_gate_topk, whose router product is not part of this call).
+ *  logits [T][E] of `dtype`, row stride ld >= E; bias fp32 [E] or NULL (zeros).
+ *  s, s' = s + bias, groups, top-k and weights as in moe_gate_topk.
+ *  - An expert whose logit or bias is -inf is masked: it is never chosen (a -inf logit
+ *    also has s = 0). A group's score is the sum of its two largest unmasked s' (its one
+ *    unmasked s'; a group without any is kept last). Where fewer than k experts can be
+ *    chosen, the remaining slots hold -1 with weight 0, and moe_permute leaves them out.
+ *  - A row with a NaN or +inf logit (or any such bias) gets -1 in every slot and NaN
+ *    weights.
+ *  - The order of s' is decided exactly: as in double precision, then by the larger
+ *    logit, then by the lower index, whatever the logits' type.
+ *  - norm_topk_prob: weights are s_j / sum s, also where every s_j lies below the fp32
+ *    range; a sum of 0 gives weights of 0.
+ *  topk_idx int32 [T][k], topk_w fp32 [T][k]. Of cfg the routing fields are used. */
+moe_status moe_route(const moe_config *cfg, int32_t dtype, const void *logits, int64_t ld,
+                     int32_t T, const float *bias, int32_t *topk_idx, float *topk_w, void *stream);
+
+/* Gradient of moe_route's topk_w with respect to the logits (the choice of experts is
+ * held; the bias has none): dlogits [T][E] of `dtype`, row stride ldd >= E, from logits
+ * (as in moe_route), topk_idx and dtopk_w fp32 [T][k].
+ *  With p_j = s of slot j's expert, G_j = routed_scaling_factor * dtopk_w_j,
+ *  norm_topk_prob: G_j <- (G_j - sum_i G_i p_i / P) / P with P = sum_i p_i; then
+ *  dl = G_j ds/dl at the chosen experts (sigmoid, sqrtsoftplus), or for the softmax
+ *  dl_e = s_e (G_e - sum_j G_j p_j) at all experts (zero for those not chosen when
+ *  norm_topk_prob). Slots with an index outside [0, E) take no part, whatever their
+ *  dtopk_w; a row without a slot that does has a zero gradient. Every element of the
+ *  T rows of dlogits is written. dlogits must not overlap logits. */
+moe_status moe_route_backward(const moe_config *cfg, int32_t dtype, const void *logits, int64_t ld,
+                              int32_t T, const int32_t *topk_idx, const float *dtopk_w,
+                              void *dlogits, int64_t ldd, void *stream);
+
+/* Gradient of moe_combine: dout bf16 [T][H]; y, row_of, topk_w as in moe_combine.
+ *  dy[row_of[t*k+j]] = bf16(topk_w[t][j] * dout[t])   (bf16 [N][H]),
+ *  dtopk_w[t][j] = sum_h dout[t][h] * y[row_of[t*k+j]][h]   (fp32 [T][k]).
+ *  A pair whose row is outside [0, N) has dtopk_w 0; rows of dy that no pair names are
+ *  left as they are. The gradient of each shared expert's output is dout itself.
+ *  dtopk_w may be NULL (y is then not read and may be NULL). dy must not overlap dout
+ *  or y. dout, y, dy 16-byte aligned. */
+moe_status moe_combine_backward(const moe_config *cfg, const void *dout, const void *y,
+                                const int32_t *row_of, const float *topk_w, int32_t T, void *dy,
+                                float *dtopk_w, void *stream);
 
 /* Byte offsets inside the workspace of the intermediate results that
  * moe_layer_forward leaves there (for inspection, tests and step-by-step use):

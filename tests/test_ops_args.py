@@ -1,0 +1,135 @@
+"""Refusals of the row operators: host checks of the C ABI and of the binding. No call
+here reaches a kernel, so none needs a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import expert_routing_grouped_layer_b200 as moe
+from expert_routing_grouped_layer_b200 import build as moe_build
+from expert_routing_grouped_layer_b200 import workloads as W
+
+BAD, UNS, WS, OK = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED, moe.MOE_ERR_WORKSPACE, moe.MOE_OK
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    moe_build.build()
+    return moe.lib()
+
+
+def test_norm(lib):
+    def f(kind=0, dt=0, x=256, ldx=64, T=4, H=64, w=256, b=256, eps=1e-6, y=256, ldy=64, mean=256, rstd=256):
+        return lib.moe_norm(kind, dt, x, ldx, T, H, w, b, ctypes.c_float(eps), y, ldy, mean, rstd, None)
+    for bad in (dict(kind=2), dict(kind=-1), dict(dt=3), dict(dt=-1), dict(x=None), dict(y=None), dict(T=-1),
+                dict(H=0), dict(eps=-1.0), dict(eps=NAN), dict(eps=INF), dict(ldx=63), dict(ldy=63),
+                dict(x=257), dict(y=257), dict(w=258), dict(b=258), dict(mean=258), dict(rstd=258),
+                dict(dt=2, x=258)):
+        assert f(**bad) == BAD, bad
+    assert f(H=16385, ldx=16385, ldy=16385) == UNS
+    assert f(T=0, x=None, y=None) == OK
+
+
+def test_norm_backward(lib):
+    need = lib.moe_norm_backward_workspace_bytes(4, 64)
+    assert need == 4 * 2 * 64 * 4  # a pair of rows per CTA, one CTA per row
+    assert lib.moe_norm_backward_workspace_bytes(-1, 64) == 0
+    assert lib.moe_norm_backward_workspace_bytes(4, 0) == 0
+    assert lib.moe_norm_backward_workspace_bytes(4, 16385) == 0
+
+    def f(kind=0, dt=0, dy=256, lddy=64, x=256, ldx=64, T=4, H=64, w=256, mean=256, rstd=256, dx=256, lddx=64,
+          dw=256, db=256, ws=256, n=need):
+        return lib.moe_norm_backward(kind, dt, dy, lddy, x, ldx, T, H, w, mean, rstd, dx, lddx, dw, db, ws, n,
+                                     None)
+    for bad in (dict(kind=3), dict(dt=7), dict(dy=None), dict(x=None), dict(T=-1), dict(H=0), dict(lddy=1),
+                dict(ldx=1), dict(lddx=1), dict(mean=None), dict(rstd=None), dict(ws=None), dict(ws=264),
+                dict(dw=257), dict(db=257), dict(dx=257), dict(dy=257), dict(w=257)):
+        assert f(**bad) == BAD, bad
+    assert f(n=need - 1) == WS
+    assert f(H=16385, ldx=16385, lddy=16385, lddx=16385) == UNS
+    assert f(dx=None, dw=None, db=None) == OK  # nothing wanted
+    assert f(kind=1, dx=None, dw=None) == OK   # the RMS norm has no bias gradient
+
+
+def _cfg(**kw):
+    return moe.make_config(W.CONFIGS["tiny_bf16"].replace(**kw))
+
+
+def test_route(lib):
+    def f(c, dt=2, l=256, ld=16, T=4, b=256, i=256, w=256):
+        return lib.moe_route(ctypes.byref(c), dt, l, ld, T, b, i, w, None)
+
+    def g(c, dt=2, l=256, ld=16, T=4, i=256, w=256, d=256, ldd=16):
+        return lib.moe_route_backward(ctypes.byref(c), dt, l, ld, T, i, w, d, ldd, None)
+    c = _cfg()
+    for bad in (dict(dt=3), dict(l=None), dict(ld=15), dict(T=-1), dict(b=257), dict(i=None), dict(w=None),
+                dict(i=258), dict(w=258), dict(l=258)):
+        assert f(c, **bad) == BAD, bad
+    for bad in (dict(dt=-1), dict(l=None), dict(ld=15), dict(T=-1), dict(i=None), dict(w=None), dict(d=None),
+                dict(ldd=15), dict(d=258), dict(i=257), dict(w=257)):
+        assert g(c, **bad) == BAD, bad
+    assert f(c, T=0, l=None) == OK and g(c, T=0, l=None) == OK
+    broken = _cfg()
+    broken.n_group = 3
+    assert f(broken) == BAD and g(broken) == BAD
+
+
+def test_combine_backward(lib):
+    def f(c, dout=256, y=256, row=256, w=256, T=4, dy=256, dw=256):
+        return lib.moe_combine_backward(ctypes.byref(c), dout, y, row, w, T, dy, dw, None)
+    c = _cfg()
+    for bad in (dict(dout=None), dict(y=None), dict(row=None), dict(w=None), dict(dy=None), dict(T=-1),
+                dict(dout=264), dict(y=264), dict(dy=264), dict(row=257), dict(w=257), dict(dw=257),
+                dict(T=0x20000000)):
+        assert f(c, **bad) == BAD, bad
+    assert f(c, T=0, dout=None) == OK
+
+
+def test_binding_refuses_before_the_library(lib):
+    """Tensors that are not on a GPU never reach a kernel; shapes, types and strides are
+    checked on the tensors themselves."""
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError, match="not on a CUDA device"):
+        moe.moe_norm(x, None, None, 1e-6, x)
+    with pytest.raises(ValueError, match="not on a CUDA device"):
+        moe.moe_route(W.CONFIGS["tiny_bf16"], torch.zeros(4, 16), None, None, None)
+    with pytest.raises(ValueError, match="not on a CUDA device"):
+        moe.moe_combine_backward(W.CONFIGS["tiny_bf16"], torch.zeros(4, 256), None, None, None, None, None)
+    with pytest.raises(ValueError, match="is missing"):
+        moe._rows("x", None)
+
+
+class _Fake:
+    """Stands for a device tensor in the binding's checks."""
+    is_cuda = True
+
+    def __init__(self, shape, stride, dtype=torch.bfloat16):
+        self.shape, self._s, self.dtype = shape, stride, dtype
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i):
+        return self._s[i]
+
+    def is_contiguous(self):
+        return False
+
+    def data_ptr(self):
+        return 4096
+
+
+def test_binding_checks_layout():
+    assert moe._rows("x", _Fake((4, 64), (72, 1))) == (4096, 72)
+    assert moe._rows("x", _Fake((1, 64), (1, 1))) == (4096, 64)
+    for shape, stride, why in [((4, 64), (64, 2), "adjacent"), ((4, 64), (32, 1), "overlap"),
+                               ((64,), (1,), "shape"), ((4, 64), (0, 1), "overlap")]:
+        with pytest.raises(ValueError, match=why):
+            moe._rows("x", _Fake(shape, stride))
+    with pytest.raises(ValueError, match="contiguous"):
+        moe._vec("w", _Fake((64,), (2,)), torch.bfloat16, (64,))
+    with pytest.raises(ValueError, match="not torch.float32"):
+        moe._vec("w", _Fake((64,), (1,)), torch.float32, (64,))
+    with pytest.raises(ValueError, match="float32 is wanted"):
+        moe._dtype("x", _Fake((4, 64), (64, 1), torch.float64))
