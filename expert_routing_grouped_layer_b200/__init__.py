@@ -26,6 +26,7 @@ SCORE_FN = {"sigmoid": 0, "sqrtsoftplus": 1, "softmax": 2}
 WFMT = {"bf16": 0, "fp8_e4m3_b128x128": 1, "fp4_e2m1_ue8m0_b32": 2, "mxfp4": 3, "nvfp4": 4}
 AFMT = {"bf16": 0, "fp8_e4m3_pow2_b128": 1, "mxfp8": 2, "nvfp4": 3}
 
+ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 NORM_KIND = {"layer": 0, "rms": 1}
 DTYPE = {"bfloat16": 0, "float16": 1, "float32": 2}  # torch dtype names
 
@@ -36,7 +37,8 @@ EXPORTS = ("moe_workspace_bytes", "moe_gate_topk", "moe_permute", "moe_quantize_
            "moe_status_string", "moe_permute_noalloc", "moe_selftest_wait_limit",
            "moe_rmsnorm_prologue", "moe_layer_forward_prenorm", "moe_norm", "moe_norm_backward",
            "moe_norm_backward_workspace_bytes", "moe_route", "moe_route_backward",
-           "moe_combine_backward")
+           "moe_combine_backward", "moe_linear", "moe_linear_backward",
+           "moe_linear_backward_workspace_bytes")
 
 # capacity (int32 counts) of the static scratch behind moe_permute_noalloc
 MOE_PERMUTE_NOALLOC_MAX_COUNTS = 262144
@@ -136,6 +138,14 @@ def lib() -> ctypes.CDLL:
             l.moe_route_backward.argtypes = [CP, _I32, _P, _I64, _I32, _P, _P, _P, _I64, _P]
             l.moe_combine_backward.restype = ctypes.c_int
             l.moe_combine_backward.argtypes = [CP, _P, _P, _P, _P, _I32, _P, _P, _P]
+            l.moe_linear.restype = ctypes.c_int
+            l.moe_linear.argtypes = [_I32, _P, _I64, _P, _I64, _P, _P, _I64, _I32, _I32, _I32, _I32, _P,
+                                     _I64, _P, _I64, _P, _P]
+            l.moe_linear_backward_workspace_bytes.restype = _SZ
+            l.moe_linear_backward_workspace_bytes.argtypes = [_I32, _I32, _I32, _I32]
+            l.moe_linear_backward.restype = ctypes.c_int
+            l.moe_linear_backward.argtypes = [_I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I32,
+                                              _I32, _I32, _P, _I64, _P, _I64, _P, _P, _SZ, _P, _P]
             _lib = l
     return _lib
 
@@ -436,6 +446,45 @@ def moe_combine_backward(cfg, dout, y, row_of, topk_w, dy, dtopk_w, stream=None)
           stream, ctypes.byref(c), _vec("dout", dout, bf, (T, H)), _vec("y", y, bf, (T * k, H)),
           _vec("row_of", row_of, torch.int32, (T * k,)), _vec("topk_w", topk_w, f, (T, k)), T,
           _vec("dy", dy, bf, (T * k, H)), _vec("dtopk_w", dtopk_w, f, (T, k)))
+
+
+def moe_linear(x, w, bias, residual, y, pre=None, act="none", dev_status=None, stream=None):
+    """y [M, N] = act(x [M, K] w [N, K]^T + bias) + residual, bf16 or f16; bias fp32 [N] or None,
+    residual [M, N] or None, pre [M, N] (None: not wanted) receives the value before act. Rows of
+    x and w start on 16-byte boundaries (strides in multiples of 8 elements)."""
+    import torch
+    M, N, K = x.shape[0], w.shape[0], x.shape[1]
+    px, ldx = _rows("x", x)
+    pw, ldw = _rows("w", w, x.dtype, (N, K))
+    py, ldy = _rows("y", y, x.dtype, (M, N))
+    pr, ldr = _rows("residual", residual, x.dtype, (M, N)) if residual is not None else (None, N)
+    pp, ldp = _rows("pre", pre, x.dtype, (M, N)) if pre is not None else (None, N)
+    _call(lib().moe_linear, "moe_linear", (x, w, bias, residual, y, pre, dev_status), stream,
+          _dtype("x", x), px, ldx, pw, ldw, _vec("bias", bias, torch.float32, (N,)), pr, ldr, ACT[act], M,
+          N, K, py, ldy, pp, ldp, _vec("dev_status", dev_status, torch.int32, (1,)))
+
+
+def moe_linear_backward_workspace_bytes(M: int, N: int, K: int, act="none") -> int:
+    return lib().moe_linear_backward_workspace_bytes(int(M), int(N), int(K), ACT[act])
+
+
+def moe_linear_backward(dy, x, w, pre, dx, dw, db, ws, act="none", dev_status=None, stream=None):
+    """Gradients of moe_linear: dx like x, dw like w, db fp32 [N]; each may be None. pre as
+    moe_linear wrote it (None for act="none"); the residual's gradient is dy. ws: at least
+    moe_linear_backward_workspace_bytes(M, N, K, act) bytes."""
+    import torch
+    M, N, K = x.shape[0], w.shape[0], x.shape[1]
+    px, ldx = _rows("x", x)
+    pw, ldw = _rows("w", w, x.dtype, (N, K))
+    pg, ldg = _rows("dy", dy, x.dtype, (M, N))
+    pp, ldp = _rows("pre", pre, x.dtype, (M, N)) if pre is not None else (None, N)
+    pdx, lddx = _rows("dx", dx, x.dtype, (M, K)) if dx is not None else (None, K)
+    pdw, lddw = _rows("dw", dw, x.dtype, (N, K)) if dw is not None else (None, K)
+    _call(lib().moe_linear_backward, "moe_linear_backward", (x, dy, w, pre, dx, dw, db, ws, dev_status),
+          stream, _dtype("x", x), pg, ldg, px, ldx, pw, ldw, pp, ldp, ACT[act], M, N, K, pdx, lddx, pdw,
+          lddw, _vec("db", db, torch.float32, (N,)), _ptr(ws),
+          0 if ws is None else ws.numel() * ws.element_size(),
+          _vec("dev_status", dev_status, torch.int32, (1,)))
 
 
 class MoELayer:

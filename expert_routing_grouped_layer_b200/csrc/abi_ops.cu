@@ -22,6 +22,21 @@ static inline bool rows_ok(const void* p, int64_t ld, int64_t cols, int dtype) {
     return p && ld >= cols && ld <= (int64_t)1 << 40 && aligned(p, dtype_size(dtype));
 }
 
+// A matrix that TMA reads: 16-byte aligned rows; the stride of a single row counts for
+// nothing.
+static inline bool tma_rows_ok(const void* p, int64_t ld, int rows, int64_t cols, int dtype) {
+    return p && aligned(p, 16) && (rows == 1 || (rows_ok(p, ld, cols, dtype) && ld % 8 == 0));
+}
+static inline int64_t tma_ld(int64_t ld, int rows, int64_t cols) { return rows == 1 ? (cols + 7) / 8 * 8 : ld; }
+
+static moe_status linear_sizes(int dtype, int act, int M, int N, int K) {
+    if (!dtype_ok(dtype) || act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH || M < 0 || N < 1 || K < 1)
+        return MOE_ERR_INVALID_ARG;
+    // sizes round up to whole tiles in 32 bits
+    if (M > 0x7fffff00 || N > 0x7fffff00 || K > 0x7fffff00) return MOE_ERR_INVALID_ARG;
+    return dtype == MOE_T_F32 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
 constexpr int kNormMaxH = 16384;
 
 extern "C" {
@@ -100,6 +115,85 @@ moe_status moe_combine_backward(const moe_config* cfg, const void* dout, const v
     if (!aligned(row_of, 4) || !aligned(topk_w, 4) || !aligned(dtopk_w, 4)) return MOE_ERR_INVALID_ARG;
     return cuda_status(launch_combine_backward(dout, y, row_of, topk_w, T, cfg->num_experts_per_tok,
                                                cfg->hidden, dy, dtopk_w, as_stream(stream)));
+}
+
+moe_status moe_linear(int32_t dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                      const float* bias, const void* residual, int64_t ldr, int32_t act, int32_t M, int32_t N,
+                      int32_t K, void* y, int64_t ldy, void* pre, int64_t ldp, int32_t* dev_status,
+                      void* stream) {
+    const moe_status st = linear_sizes(dtype, act, M, N, K);
+    if (st != MOE_OK || M == 0) return st;
+    if (!tma_rows_ok(x, ldx, M, K, dtype) || !tma_rows_ok(w, ldw, N, K, dtype)) return MOE_ERR_INVALID_ARG;
+    if (!rows_ok(y, ldy, N, dtype)) return MOE_ERR_INVALID_ARG;
+    if ((residual && !rows_ok(residual, ldr, N, dtype)) || (pre && !rows_ok(pre, ldp, N, dtype)))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(bias, 4) || !aligned(dev_status, 4)) return MOE_ERR_INVALID_ARG;
+    LinearArgs a{};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.act = act;
+    a.x = x;
+    a.ldx = tma_ld(ldx, M, K);
+    a.w = w;
+    a.ldw = tma_ld(ldw, N, K);
+    a.bias = bias;
+    a.res = residual;
+    a.ldr = ldr;
+    a.y = y;
+    a.ldy = ldy;
+    a.pre = pre;
+    a.ldp = ldp;
+    a.status = dev_status;
+    return cuda_status(launch_linear(dtype, a, as_stream(stream)));
+}
+
+size_t moe_linear_backward_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t act) {
+    if (linear_sizes(MOE_T_BF16, act, M, N, K) != MOE_OK) return 0;
+    return linear_backward_ws(M, N);
+}
+
+moe_status moe_linear_backward(int32_t dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                               const void* w, int64_t ldw, const void* pre, int64_t ldp, int32_t act, int32_t M,
+                               int32_t N, int32_t K, void* dx, int64_t lddx, void* dw, int64_t lddw, float* db,
+                               void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+    const moe_status st = linear_sizes(dtype, act, M, N, K);
+    if (st != MOE_OK) return st;
+    if (!dx && !dw && !db) return MOE_OK;
+    if ((dw && !rows_ok(dw, lddw, K, dtype)) || !aligned(db, 4) || !aligned(dev_status, 4)) return MOE_ERR_INVALID_ARG;
+    if (M == 0) {  // no rows: the sums are zero
+        cudaError_t e = cudaSuccess;
+        if (dw) e = cudaMemset2DAsync(dw, (size_t)lddw * 2, 0, (size_t)K * 2, N, as_stream(stream));
+        if (db && e == cudaSuccess) e = cudaMemsetAsync(db, 0, (size_t)N * 4, as_stream(stream));
+        return cuda_status(e);
+    }
+    if (!rows_ok(dy, lddy, N, dtype)) return MOE_ERR_INVALID_ARG;
+    if (act != MOE_ACT_NONE && !rows_ok(pre, ldp, N, dtype)) return MOE_ERR_INVALID_ARG;
+    if (dx && (!rows_ok(dx, lddx, K, dtype) || !tma_rows_ok(w, ldw, N, K, dtype))) return MOE_ERR_INVALID_ARG;
+    if (dw && !tma_rows_ok(x, ldx, M, K, dtype)) return MOE_ERR_INVALID_ARG;
+    if (!ws || !aligned(ws, 16)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < linear_backward_ws(M, N)) return MOE_ERR_WORKSPACE;
+    LinearArgs a{};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.act = act;
+    a.dy = dy;
+    a.lddy = M == 1 ? tma_ld(lddy, M, N) : lddy;
+    a.x = x;
+    a.ldx = tma_ld(ldx, M, K);
+    a.w = w;
+    a.ldw = tma_ld(ldw, N, K);
+    a.pre = const_cast<void*>(pre);
+    a.ldp = ldp;
+    a.dx = dx;
+    a.lddx = lddx;
+    a.dw = dw;
+    a.lddw = lddw;
+    a.db = db;
+    a.ws = ws;
+    a.status = dev_status;
+    return cuda_status(launch_linear_backward(dtype, a, as_stream(stream)));
 }
 
 }  // extern "C"

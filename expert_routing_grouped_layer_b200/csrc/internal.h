@@ -125,6 +125,21 @@ cudaError_t launch_combine_backward(const void* dout, const void* y, const int32
                                     const float* w, int T, int k, int H, void* dy, float* dw,
                                     cudaStream_t st);
 
+// Dense linear layer (linear.cu): y = act(x W^T + bias) + residual and its gradients.
+struct LinearArgs {
+    int M, N, K, act;
+    const void *x, *w, *res, *dy;
+    const float* bias;
+    void *y, *pre, *dx, *dw;  // pre: output of the forward, input of the backward pass
+    float* db;
+    long ldx, ldw, ldr, ldy, ldp, lddy, lddx, lddw;
+    void* ws;
+    int32_t* status;
+};
+cudaError_t launch_linear(int dtype, const LinearArgs& a, cudaStream_t st);
+size_t linear_backward_ws(int M, int N);
+cudaError_t launch_linear_backward(int dtype, const LinearArgs& a, cudaStream_t st);
+
 struct GroupedGemmArgs {
     // problem
     int gemm;           // 1: gate/up + SwiGLU, 2: down projection

@@ -27,6 +27,11 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+template <typename T>
+__host__ __device__ constexpr bool is_half() { return false; }
+template <>
+__host__ __device__ constexpr bool is_half<__half>() { return true; }
+
 // VEC consecutive elements, moved by one access where they fill 16 bytes.
 template <typename T, int VEC>
 struct alignas(sizeof(T) * VEC) Pack {

@@ -121,6 +121,14 @@ typedef enum {
 #define MOE_T_F16 1
 #define MOE_T_F32 2
 
+/* activations of moe_linear: y = z, max(z, 0), z * sigmoid(z), z * Phi(z) (erf), and the
+ * tanh form z/2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))) */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_SILU 2
+#define MOE_ACT_GELU 3
+#define MOE_ACT_GELU_TANH 4
+
 /* norm kinds */
 #define MOE_NORM_LAYER 0
 #define MOE_NORM_RMS 1
@@ -406,6 +414,41 @@ moe_status moe_route_backward(const moe_config *cfg, int32_t dtype, const void *
 moe_status moe_combine_backward(const moe_config *cfg, const void *dout, const void *y,
                                 const int32_t *row_of, const float *topk_w, int32_t T, void *dy,
                                 float *dtopk_w, void *stream);
+
+/* Dense linear layer (the decoder layer's projections and dense feed-forward blocks
+ * around the experts): z = x W^T + bias, y = act(z) + residual.
+ *  x [M][K], w [N][K] of `dtype` (MOE_T_BF16 or MOE_T_F16; MOE_T_F32 returns
+ *  MOE_ERR_UNSUPPORTED), row strides in elements, multiples of 8, 16-byte aligned bases
+ *  (the stride of a single row is not used); M, N, K need no alignment. bias fp32 [N] or
+ *  NULL; residual [M][N] or NULL; y [M][N]; pre [M][N] receives z rounded to `dtype` (for
+ *  the backward pass) or is NULL; these three may have any stride >= N and any alignment
+ *  of their elements. y may be residual when the strides are equal; no other output may
+ *  overlap an input. act MOE_ACT_*. Products accumulate in fp32 (a NaN or infinity in x
+ *  or w reaches the rows and columns it belongs to); y is rounded once. The order of the
+ *  additions depends on the sizes and the GPU alone. MOE_DEV_TIMEOUT in *dev_status (may
+ *  be NULL) if a pipeline wait ran out. M = 0 does nothing; N, K >= 1. */
+moe_status moe_linear(int32_t dtype, const void *x, int64_t ldx, const void *w, int64_t ldw,
+                      const float *bias, const void *residual, int64_t ldr, int32_t act, int32_t M,
+                      int32_t N, int32_t K, void *y, int64_t ldy, void *pre, int64_t ldp,
+                      int32_t *dev_status, void *stream);
+
+/* Gradients of moe_linear: with g = dy * act'(pre),
+ *  dx = g W  [M][K],  dw = g^T x  [N][K],  db = sum_m g  (fp32 [N]);
+ *  the residual's gradient is dy itself. dx, dw, db may each be NULL (not wanted).
+ *  dy, pre [M][N] of `dtype`: pre as moe_linear wrote it, NULL allowed for MOE_ACT_NONE.
+ *  x and w as in moe_linear; dy, pre, dx, dw may have any stride >= their width and any
+ *  alignment of their elements. g is rounded to `dtype` between the elementwise step and
+ *  the products (not in db); dx and dw are rounded once and overwritten; M = 0 sets dw
+ *  and db to zero. Outputs must not overlap inputs. ws: 16-byte aligned,
+ *  moe_linear_backward_workspace_bytes bytes. */
+moe_status moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void *x,
+                               int64_t ldx, const void *w, int64_t ldw, const void *pre,
+                               int64_t ldp, int32_t act, int32_t M, int32_t N, int32_t K, void *dx,
+                               int64_t lddx, void *dw, int64_t lddw, float *db, void *ws,
+                               size_t ws_bytes, int32_t *dev_status, void *stream);
+
+/* Workspace of moe_linear_backward; 0 for invalid sizes. */
+size_t moe_linear_backward_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t act);
 
 /* Byte offsets inside the workspace of the intermediate results that
  * moe_layer_forward leaves there (for inspection, tests and step-by-step use):

@@ -94,3 +94,31 @@ def combine_backward(dout, y, row_of, w, dy):
             dy[row] = w[t, j].double() * dout[t]
             dw[t, j] = (dout[t] * y[row].double()).sum()
     return dy, dw
+
+
+def act(z, name):
+    if name == "relu":
+        return z.clamp(min=0)
+    if name == "silu":
+        return z * torch.sigmoid(z)
+    if name == "gelu":
+        return 0.5 * z * torch.special.erfc(-z * math.sqrt(0.5))
+    if name == "gelu_tanh":
+        return 0.5 * z * (1 + torch.tanh(math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)))
+    return z
+
+
+def linear(x, w, bias, residual, name):
+    z = x.double() @ w.double().t()
+    if bias is not None:
+        z = z + bias.double()
+    y = act(z, name)
+    return z, y if residual is None else y + residual.double()
+
+
+def linear_backward(dy, x, w, pre, name):
+    g = dy.double()
+    if name != "none":
+        z = pre.double().clone().requires_grad_(True)
+        g = torch.autograd.grad(act(z, name), z, g)[0]
+    return g, g @ w.double(), g.t() @ x.double(), g.sum(0)

@@ -1,0 +1,235 @@
+"""moe_linear and moe_linear_backward against the 64-bit formulas.
+
+Tolerances. The tensor cores add K products in steps of 16, each step off by at most one
+unit of 2^-23 of the sum of magnitudes, plus a tree of partial sums: (K / 16 + 16) 2^-23
+sum |x w|. The activations' slopes are below 1.13, their own evaluation is off by at most
+2^-21 (1 + |z|). Rounding to the output's type: half a step. In the backward pass g is
+rounded to the type before the products."""
+import pytest
+import torch
+
+import expert_routing_grouped_layer_b200 as moe
+import ops_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
+TINY = {HF: 2.0 ** -25, BF: 1e-38}  # half of fp16's smallest step
+
+
+def acc_unit(K):
+    return (K / 16 + 16) * 2.0 ** -23
+
+
+def _mat(g, rows, cols, dt, pad=True, scale=1.0):
+    ld = (cols + 7) // 8 * 8 if pad else cols
+    return (torch.randn(rows, ld, generator=g, device="cuda") * scale).to(dt)[:, :cols]
+
+
+def _forward(M, N, K, dt, act="none", bias=True, residual=False, pre=False, seed=0, check=True, out_ld=None):
+    g = torch.Generator(device="cuda").manual_seed(seed + M + N + K)
+    x, w = _mat(g, M, K, dt), _mat(g, N, K, dt, scale=K ** -0.5)
+    b = torch.randn(N, generator=g, device="cuda") if bias else None
+    r = _mat(g, M, N, dt, pad=out_ld is None) if residual else None
+    y = torch.full((M, out_ld or N), 77.0, dtype=dt, device="cuda")
+    z = torch.full((M, out_ld or N), 77.0, dtype=dt, device="cuda") if pre else None
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    moe.moe_linear(x, w, b, r, y[:, :N], z[:, :N] if pre else None, act=act, dev_status=st)
+    assert st.item() == 0
+    if check:
+        zd, yd = ref.linear(x, w, b, r, act)
+        mag = x.double().abs() @ w.double().abs().t() + (b.double().abs() if bias else 0)
+        err = acc_unit(K) * mag
+        if pre:
+            assert ((z[:, :N].double() - zd).abs() <= ref.U[dt] * zd.abs() + err * 1.01 + TINY[dt]).all()
+        ev = 1.13 * err + 2.0 ** -21 * (1 + zd.abs()) + 2.0 ** -23 * (r.double().abs() if residual else 0)
+        bad = (y[:, :N].double() - yd).abs() > ref.U[dt] * yd.abs() + 1.01 * ev + TINY[dt]
+        assert not bad.any(), (int(bad.sum()), bad.nonzero()[:3].tolist())
+        assert (y[:, N:] == 77).all()
+    return x, w, b, r, y, z
+
+
+SIZES = [(1, 1, 1), (1, 128, 64), (1, 2048, 7168), (1, 300, 515), (2, 7168, 2048), (3, 5, 7), (15, 130, 100),
+         (16, 384, 7168), (17, 257, 66), (64, 640, 1024), (80, 1000, 72), (96, 2048, 512), (127, 129, 65),
+         (128, 7168, 2048), (129, 256, 192), (200, 96, 4097), (256, 4096, 256), (257, 300, 700),
+         (512, 2048, 1024), (700, 512, 2048), (1037, 2051, 1111), (2048, 2048, 2048), (5000, 100, 40),
+         (4096, 16, 128), (9, 20000, 64), (3000, 1500, 1000), (1111, 7168, 64)]
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_sizes(M, N, K, dt):
+    _forward(M, N, K, dt)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 200, 333), (300, 515, 128), (2048, 1024, 512)])
+@pytest.mark.parametrize("act", list(moe.ACT))
+def test_epilogue(M, N, K, act):
+    _forward(M, N, K, BF, act, residual=True, pre=True)
+    _forward(M, N, K, HF, act, bias=False, pre=True)
+    _forward(M, N, K, BF, act, bias=False, residual=True)
+
+
+@pytest.mark.parametrize("M,N,out_ld", [(33, 100, 101), (33, 101, 101), (600, 514, 517), (600, 512, 516)])
+def test_output_strides(M, N, out_ld):
+    """Outputs and residuals whose rows allow no wide accesses; what lies between stays."""
+    _forward(M, N, 96, BF, "silu", residual=True, pre=True, out_ld=out_ld)
+
+
+def test_residual_in_place_and_equal_bits():
+    for M, N, K in [(4, 512, 2048), (3000, 1024, 512)]:
+        x, w, b, r, y, _ = _forward(M, N, K, BF, "none", residual=True, seed=1)
+        h = r.clone()
+        moe.moe_linear(x, w, b, h, h)
+        assert torch.equal(h, y)
+        for _ in range(3):
+            again = torch.empty_like(y)
+            moe.moe_linear(x, w, b, r, again)
+            assert torch.equal(again, y)
+
+
+def test_values_outside_the_matrices_stay_outside():
+    """NaN in the padding of x's and w's rows and behind their last rows reaches nothing;
+    NaN and infinities inside reach their own rows and columns."""
+    for M, N, K in [(20, 140, 70), (300, 600, 70)]:
+        g = torch.Generator(device="cuda").manual_seed(2)
+        xa = torch.full((M + 5, 80), float("nan"), dtype=BF, device="cuda")
+        wa = torch.full((N + 5, 80), float("nan"), dtype=BF, device="cuda")
+        xa[:M, :K] = torch.randn(M, K, generator=g, device="cuda").to(BF)
+        wa[:N, :K] = torch.randn(N, K, generator=g, device="cuda").to(BF)
+        x, w = xa[:M, :K], wa[:N, :K]
+        y = torch.empty(M, N, dtype=BF, device="cuda")
+        moe.moe_linear(x, w, None, None, y)
+        assert torch.isfinite(y).all()
+        x[3, 5] = float("nan")
+        w[7, 0] = float("inf")
+        for act in ("none", "relu"):
+            moe.moe_linear(x, w, None, None, y, act=act)
+            assert torch.isnan(y[3]).all()
+            keep = torch.ones(M, dtype=torch.bool, device="cuda")
+            keep[3] = False
+            z = x[keep].double() @ w.double().t()
+            want = z[:, 7].clamp(min=0) if act == "relu" else z[:, 7]
+            assert torch.equal(y[keep][:, 7].double(), want)
+            cols = torch.ones(N, dtype=torch.bool, device="cuda")
+            cols[7] = False
+            assert torch.isfinite(y[keep][:, cols]).all()
+
+
+def _backward(M, N, K, dt, act, seed=0, dy_pad=True, want=(True, True, True)):
+    g = torch.Generator(device="cuda").manual_seed(seed + M + N + K)
+    x, w = _mat(g, M, K, dt), _mat(g, N, K, dt, scale=K ** -0.5)
+    dy, pre = _mat(g, M, N, dt, pad=dy_pad), _mat(g, M, N, dt, pad=dy_pad)
+    dx = torch.full((M, K), 7.0, dtype=dt, device="cuda") if want[0] else None
+    dw = torch.full((N, K), 7.0, dtype=dt, device="cuda") if want[1] else None
+    db = torch.full((N,), 7.0, device="cuda") if want[2] else None
+    ws = torch.empty(moe.moe_linear_backward_workspace_bytes(M, N, K, act), dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    p = pre if act != "none" else None
+    moe.moe_linear_backward(dy, x, w, p, dx, dw, db, ws, act=act, dev_status=st)
+    assert st.item() == 0
+    gd, rdx, rdw, rdb = ref.linear_backward(dy, x, w, p, act)
+    slope = 2.0 ** -21 * dy.double().abs() * (1 + pre.double().abs()) if act != "none" else 0 * gd
+    dg = slope + ref.U[dt] * gd.abs() + TINY[dt]
+    ga, wa, xa = gd.abs(), w.double().abs(), x.double().abs()
+    if want[0]:
+        tol = dg @ wa + acc_unit(N) * 1.01 * (ga @ wa) + ref.U[dt] * rdx.abs() * 1.01 + TINY[dt]
+        assert ((dx.double() - rdx).abs() <= tol).all()
+    if want[1]:
+        tol = dg.t() @ xa + acc_unit(M) * 1.01 * (ga.t() @ xa) + ref.U[dt] * rdw.abs() * 1.01 + TINY[dt]
+        assert ((dw.double() - rdw).abs() <= tol).all()
+    if want[2]:  # at most 64 rows a warp (M <= 32768), 8 warps, 8 x 8 chunks
+        assert ((db.double() - rdb).abs() <= slope.sum(0) + 96 * 2.0 ** -24 * ga.sum(0)).all()
+    return x, w, dy, pre, dx, dw, db
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 200, 300), (3, 5, 7), (16, 128, 128), (33, 100, 515),
+                                   (65, 64, 7168), (128, 2048, 512), (200, 1000, 129), (300, 515, 700),
+                                   (1037, 300, 411), (5000, 100, 40), (777, 2048, 1024), (2048, 2048, 2048),
+                                   (4100, 64, 64)])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_backward(M, N, K, dt):
+    _backward(M, N, K, dt, "silu")
+    _backward(M, N, K, dt, "none", seed=1)
+
+
+@pytest.mark.parametrize("act", list(moe.ACT))
+def test_backward_activations_and_strides(act):
+    _backward(100, 101, 96, BF, act, dy_pad=False)
+    _backward(515, 264, 130, HF, act)
+    for want in ((True, False, False), (False, True, False), (False, False, True)):
+        _backward(70, 90, 50, BF, act, want=want)
+
+
+def test_gradients_against_differences():
+    """The forward's own formula, evaluated either side of a value."""
+    for act in moe.ACT:
+        x, w, dy, pre, dx, dw, db = _backward(4, 6, 8, BF, act, seed=3)
+        b = pre.double() - x.double() @ w.double().t()  # a bias per element that gives this pre
+        f = lambda x_, w_: (ref.act(x_ @ w_.t() + b, act) * dy.double()).sum().item()
+        h = 1e-6
+        for t, i, j in [(0, 1, 2), (3, 5, 7)]:
+            d = torch.zeros(4, 8, dtype=torch.float64, device="cuda")
+            d[t, j] = h
+            num = (f(x.double() + d, w.double()) - f(x.double() - d, w.double())) / (2 * h)
+            # bf16: g and the result are rounded, 2^-8 of the terms each
+            terms = (dy[t].double().abs() * w[:, j].double().abs()).sum().item()
+            assert abs(num - dx[t, j].item()) <= 2.5 * 2.0 ** -8 * terms + 1e-4
+            e = torch.zeros(6, 8, dtype=torch.float64, device="cuda")
+            e[i, j] = h
+            num = (f(x.double(), w.double() + e) - f(x.double(), w.double() - e)) / (2 * h)
+            terms = (dy[:, i].double().abs() * x[:, j].double().abs()).sum().item()
+            assert abs(num - dw[i, j].item()) <= 2.5 * 2.0 ** -8 * terms + 1e-4
+
+
+def test_no_rows():
+    w = torch.ones(6, 16, dtype=BF, device="cuda")
+    x = torch.empty(0, 16, dtype=BF, device="cuda")
+    y = torch.empty(0, 6, dtype=BF, device="cuda")
+    moe.moe_linear(x, w, None, None, y)
+    wide = torch.full((6, 20), 3.0, dtype=BF, device="cuda")
+    db = torch.ones(6, device="cuda")
+    moe.moe_linear_backward(y, x, w, None, x, wide[:, :16], db, None)
+    assert (wide[:, :16] == 0).all() and (wide[:, 16:] == 3).all() and (db == 0).all()
+
+
+def test_two_streams_and_graphs():
+    """The same layer on two streams at once, and captured graphs replayed on new inputs."""
+    M, N, K = 96, 1024, 2048
+    runs = []
+    for seed in (5, 6):
+        s = torch.cuda.Stream()
+        x, w, b, r, y, z = _forward(M, N, K, BF, "gelu", residual=True, pre=True, seed=seed)
+        dy = torch.randn(M, N, device="cuda").to(BF)
+        out = [torch.empty_like(y), torch.empty_like(z), torch.empty_like(x), torch.empty_like(w),
+               torch.empty(N, device="cuda")]
+        ws = torch.empty(moe.moe_linear_backward_workspace_bytes(M, N, K, "gelu"), dtype=torch.uint8,
+                         device="cuda")
+
+        def step(stream=None, x=x, w=w, b=b, r=r, out=out, dy=dy, ws=ws):
+            moe.moe_linear(x, w, b, r, out[0], out[1], act="gelu", stream=stream)
+            moe.moe_linear_backward(dy, x, w, out[1], out[2], out[3], out[4], ws, act="gelu", stream=stream)
+        step()
+        torch.cuda.synchronize()
+        runs.append((s, step, out, [o.clone() for o in out], x))
+    for _ in range(20):
+        for s, step, *_ in runs:
+            step(s)
+    torch.cuda.synchronize()
+    for s, step, out, want, x in runs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    graphs = []
+    for s, step, out, want, x in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step()
+        x.neg_()
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    for s, step, out, want, x in runs:
+        got = [o.clone() for o in out]
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, out))

@@ -86,6 +86,39 @@ def test_combine_backward(lib):
     assert f(c, T=0, dout=None) == OK
 
 
+def test_linear(lib):
+    def f(dt=0, x=256, ldx=64, w=256, ldw=64, b=256, r=256, ldr=32, act=0, M=4, N=32, K=64, y=256, ldy=32, p=256,
+          ldp=32, st=None):
+        return lib.moe_linear(dt, x, ldx, w, ldw, b, r, ldr, act, M, N, K, y, ldy, p, ldp, st, None)
+    for bad in (dict(dt=3), dict(x=None), dict(w=None), dict(y=None), dict(M=-1), dict(N=0), dict(K=0),
+                dict(act=5), dict(act=-1), dict(ldx=60), dict(ldw=68), dict(ldx=56), dict(x=264), dict(w=264),
+                dict(ldy=31), dict(ldr=31), dict(ldp=31), dict(y=257), dict(r=257), dict(p=257), dict(b=258),
+                dict(st=257), dict(M=0x7fffffff)):
+        assert f(**bad) == BAD, bad
+    assert f(dt=2) == UNS  # fp32 operands
+    assert f(M=0, x=None) == OK
+
+
+def test_linear_backward(lib):
+    need = lib.moe_linear_backward_workspace_bytes(4, 32, 64, 0)
+    assert need >= 4 * 32 * 2 + 32 * 4
+    assert lib.moe_linear_backward_workspace_bytes(4, 0, 64, 0) == 0
+    assert lib.moe_linear_backward_workspace_bytes(4, 32, 64, 9) == 0
+
+    def f(dt=0, dy=256, lddy=32, x=256, ldx=64, w=256, ldw=64, p=256, ldp=32, act=2, M=4, N=32, K=64, dx=256,
+          lddx=64, dw=256, lddw=64, db=256, ws=256, n=need, st=None):
+        return lib.moe_linear_backward(dt, dy, lddy, x, ldx, w, ldw, p, ldp, act, M, N, K, dx, lddx, dw, lddw, db,
+                                       ws, n, st, None)
+    for bad in (dict(dt=9), dict(dy=None), dict(x=None), dict(w=None), dict(p=None), dict(act=7), dict(M=-1),
+                dict(N=0), dict(K=0), dict(lddy=31), dict(ldx=60), dict(ldw=60), dict(ldp=31), dict(lddx=63),
+                dict(lddw=63), dict(x=264), dict(w=264), dict(dx=257), dict(dw=257), dict(db=257), dict(ws=None),
+                dict(ws=264), dict(st=258), dict(p=257)):
+        assert f(**bad) == BAD, bad
+    assert f(n=need - 1) == WS
+    assert f(dt=2) == UNS
+    assert f(dx=None, dw=None, db=None) == OK
+
+
 def test_binding_refuses_before_the_library(lib):
     """Tensors that are not on a GPU never reach a kernel; shapes, types and strides are
     checked on the tensors themselves."""
