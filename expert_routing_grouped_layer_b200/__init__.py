@@ -83,6 +83,8 @@ _F32 = ctypes.c_float
 def lib() -> ctypes.CDLL:
     """Load libmoe.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -322,73 +324,99 @@ def moe_layer_forward_prenorm(cfg, x, T, norm_w, eps, weights, out, ws, dev_stat
 
 # The operators below take tensors and read sizes, strides and types from them. The
 # tensors have to lie on one CUDA device, which is current during the call; without a
-# `stream` the call goes to that device's current stream.
-def _rows(name, t, dtype=None, shape=None):
-    """(address, row stride) of a row-major matrix whose rows are dense."""
-    _tensor(name, t, dtype, shape, 2)
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError("%s: the elements of a row must be adjacent" % name)
-    # a single row's stride is never used
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-    if ld < t.shape[1]:
-        raise ValueError("%s: rows overlap (stride %d, %d columns)" % (name, ld, t.shape[1]))
+# `stream` the call goes to that device's current stream. These checks run on every call,
+# so they are written for few Python operations (a call takes about 6 us of host time).
+def _rows(name, t, dev, dtype, shape):
+    """(address, row stride) of a row-major matrix on device `dev` whose rows are dense."""
+    if t is None or t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _refuse(name, t, dev, dtype, shape)
+    ld, step = t.stride()
+    rows, cols = shape
+    if rows <= 1:  # the stride of a single row is never used
+        ld = max(ld, cols)
+    if (step != 1 and cols > 1) or ld < cols:
+        raise ValueError("%s: strides %s; the elements of a row must be adjacent and rows must not overlap"
+                         % (name, t.stride()))
     return t.data_ptr(), ld
 
 
-def _vec(name, t, dtype, shape):
-    """Address of a contiguous tensor, or None for None."""
+def _vec(name, t, dev, dtype, shape):
+    """Address of a contiguous tensor on device `dev`, or None for None."""
     if t is None:
         return None
-    _tensor(name, t, dtype, shape, len(shape))
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _refuse(name, t, dev, dtype, shape)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
 
 
-def _tensor(name, t, dtype, shape, ndim):
+def _bytes(name, t, dev):
+    """(address, size in bytes) of a workspace on device `dev`; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be contiguous and on device %d" % (name, dev))
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _refuse(name, t, dev, dtype, shape):
     if t is None:
         raise ValueError("%s is missing" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, not on CUDA device %d" % (name, t.device, dev))
+    if t.dtype is not dtype:
+        raise ValueError("%s is %s, not %s" % (name, t.dtype, dtype))
+    raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+def _matrix(name, t):
+    """(device index, MOE_T_* type, shape) of a call's first operand."""
     if not t.is_cuda:
         raise ValueError("%s is not on a CUDA device" % name)
-    if t.dim() != ndim or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape),
-                                                      shape if shape is not None else "%d-d" % ndim))
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError("%s is %s, not %s" % (name, t.dtype, dtype))
-
-
-def _dtype(name, t) -> int:
-    d = DTYPE.get(str(t.dtype).replace("torch.", ""))
+    if t.dim() != 2:
+        raise ValueError("%s has shape %s: a matrix is wanted" % (name, tuple(t.shape)))
+    d = _dtypes().get(t.dtype)
     if d is None:
         raise ValueError("%s is %s: bfloat16, float16 or float32 is wanted" % (name, t.dtype))
-    return d
+    return t.get_device(), d, t.shape
 
 
-def _call(fn, where, tensors, stream, *args):
-    """fn(*args, stream) with the tensors' device current."""
+_dtype_of: dict = {}
+
+
+def _dtypes() -> dict:
+    if not _dtype_of:
+        import torch
+        _dtype_of.update({getattr(torch, n): v for n, v in DTYPE.items()})
+    return _dtype_of
+
+
+def _call(fn, where, dev, stream, *args):
+    """fn(*args, stream) with device `dev` current."""
     import torch
-    dev = tensors[0].device
-    for t in tensors[1:]:
-        if t is not None and t.device != dev:
-            raise ValueError("%s: tensors on %s and %s" % (where, dev, t.device))
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), where)
-    else:
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)), where)
+            s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+            status = fn(*args, s)
+    else:
+        s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+        status = fn(*args, s)
+    if status != MOE_OK:
+        raise MoEError(status, where)
 
 
 def moe_norm(x, w, b, eps, y, mean=None, rstd=None, kind="layer", stream=None):
     """Layer norm (or RMS norm, kind="rms") of the rows of x [T, H] into y; w and b fp32
     [H] or None; mean and rstd fp32 [T] are filled where given."""
-    import torch
-    T, H = x.shape
-    px, ldx = _rows("x", x)
-    py, ldy = _rows("y", y, x.dtype, (T, H))
-    f = torch.float32
-    _call(lib().moe_norm, "moe_norm", (x, y, w, b, mean, rstd), stream, NORM_KIND[kind],
-          _dtype("x", x), px, ldx, T, H, _vec("w", w, f, (H,)), _vec("b", b, f, (H,)), float(eps), py,
-          ldy, _vec("mean", mean, f, (T,)), _vec("rstd", rstd, f, (T,)))
+    from torch import float32 as f
+    dev, dt, shape = _matrix("x", x)
+    T, H = shape
+    px, ldx = _rows("x", x, dev, x.dtype, shape)
+    py, ldy = _rows("y", y, dev, x.dtype, shape)
+    _call(lib().moe_norm, "moe_norm", dev, stream, NORM_KIND[kind], dt, px, ldx, T, H,
+          _vec("w", w, dev, f, (H,)), _vec("b", b, dev, f, (H,)), eps, py, ldy,
+          _vec("mean", mean, dev, f, (T,)), _vec("rstd", rstd, dev, f, (T,)))
 
 
 def moe_norm_backward_workspace_bytes(T: int, H: int) -> int:
@@ -398,70 +426,72 @@ def moe_norm_backward_workspace_bytes(T: int, H: int) -> int:
 def moe_norm_backward(dy, x, w, mean, rstd, dx, dw, db, ws, kind="layer", stream=None):
     """Gradients of moe_norm: dx [T, H] like x, dw and db fp32 [H]; each may be None. ws: at
     least moe_norm_backward_workspace_bytes(T, H) bytes (None without dw and db)."""
-    import torch
-    T, H = x.shape
-    px, ldx = _rows("x", x)
-    pg, ldg = _rows("dy", dy, x.dtype, (T, H))
-    pd, ldd = _rows("dx", dx, x.dtype, (T, H)) if dx is not None else (None, H)
-    f = torch.float32
-    _call(lib().moe_norm_backward, "moe_norm_backward", (x, dy, w, mean, rstd, dx, dw, db, ws), stream,
-          NORM_KIND[kind], _dtype("x", x), pg, ldg, px, ldx, T, H, _vec("w", w, f, (H,)),
-          _vec("mean", mean, f, (T,)), _vec("rstd", rstd, f, (T,)), pd, ldd, _vec("dw", dw, f, (H,)),
-          _vec("db", db, f, (H,)), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+    from torch import float32 as f
+    dev, dt, shape = _matrix("x", x)
+    T, H = shape
+    px, ldx = _rows("x", x, dev, x.dtype, shape)
+    pg, ldg = _rows("dy", dy, dev, x.dtype, shape)
+    pd, ldd = _rows("dx", dx, dev, x.dtype, shape) if dx is not None else (None, H)
+    pws, nws = _bytes("ws", ws, dev)
+    _call(lib().moe_norm_backward, "moe_norm_backward", dev, stream, NORM_KIND[kind], dt, pg, ldg, px,
+          ldx, T, H, _vec("w", w, dev, f, (H,)), _vec("mean", mean, dev, f, (T,)),
+          _vec("rstd", rstd, dev, f, (T,)), pd, ldd, _vec("dw", dw, dev, f, (H,)),
+          _vec("db", db, dev, f, (H,)), pws, nws)
 
 
 def moe_route(cfg, logits, bias, topk_idx, topk_w, stream=None):
     """Experts and weights from router logits [T, E] (bf16, f16 or fp32) and a balance bias
     fp32 [E] or None: topk_idx int32 [T, k], topk_w fp32 [T, k]."""
-    import torch
+    from torch import float32 as f, int32 as i
     c = _cfg(cfg)
-    T, k, E = logits.shape[0], c.num_experts_per_tok, c.n_routed_experts
-    p, ld = _rows("logits", logits, None, (T, E))
-    _call(lib().moe_route, "moe_route", (logits, bias, topk_idx, topk_w), stream, ctypes.byref(c),
-          _dtype("logits", logits), p, ld, T, _vec("bias", bias, torch.float32, (E,)),
-          _vec("topk_idx", topk_idx, torch.int32, (T, k)), _vec("topk_w", topk_w, torch.float32, (T, k)))
+    dev, dt, shape = _matrix("logits", logits)
+    T, k, E = shape[0], c.num_experts_per_tok, c.n_routed_experts
+    p, ld = _rows("logits", logits, dev, logits.dtype, (T, E))
+    _call(lib().moe_route, "moe_route", dev, stream, c, dt, p, ld, T, _vec("bias", bias, dev, f, (E,)),
+          _vec("topk_idx", topk_idx, dev, i, (T, k)), _vec("topk_w", topk_w, dev, f, (T, k)))
 
 
 def moe_route_backward(cfg, logits, topk_idx, dtopk_w, dlogits, stream=None):
     """dlogits [T, E], like logits, from the gradient dtopk_w fp32 [T, k] of moe_route's weights."""
-    import torch
+    from torch import float32 as f, int32 as i
     c = _cfg(cfg)
-    T, k, E = logits.shape[0], c.num_experts_per_tok, c.n_routed_experts
-    p, ld = _rows("logits", logits, None, (T, E))
-    pd, ldd = _rows("dlogits", dlogits, logits.dtype, (T, E))
-    _call(lib().moe_route_backward, "moe_route_backward", (logits, topk_idx, dtopk_w, dlogits), stream,
-          ctypes.byref(c), _dtype("logits", logits), p, ld, T,
-          _vec("topk_idx", topk_idx, torch.int32, (T, k)),
-          _vec("dtopk_w", dtopk_w, torch.float32, (T, k)), pd, ldd)
+    dev, dt, shape = _matrix("logits", logits)
+    T, k, E = shape[0], c.num_experts_per_tok, c.n_routed_experts
+    p, ld = _rows("logits", logits, dev, logits.dtype, (T, E))
+    pd, ldd = _rows("dlogits", dlogits, dev, logits.dtype, (T, E))
+    _call(lib().moe_route_backward, "moe_route_backward", dev, stream, c, dt, p, ld, T,
+          _vec("topk_idx", topk_idx, dev, i, (T, k)), _vec("dtopk_w", dtopk_w, dev, f, (T, k)), pd, ldd)
 
 
 def moe_combine_backward(cfg, dout, y, row_of, topk_w, dy, dtopk_w, stream=None):
     """Gradients of moe_combine: dy bf16 [N, H] (rows of dropped pairs stay as they are) and
     dtopk_w fp32 [T, k] (None: not wanted, y may then be None)."""
-    import torch
+    from torch import bfloat16 as h, float32 as f, int32 as i
     c = _cfg(cfg)
-    T, k, H = dout.shape[0], c.num_experts_per_tok, c.hidden
-    bf, f = torch.bfloat16, torch.float32
-    _call(lib().moe_combine_backward, "moe_combine_backward", (dout, y, row_of, topk_w, dy, dtopk_w),
-          stream, ctypes.byref(c), _vec("dout", dout, bf, (T, H)), _vec("y", y, bf, (T * k, H)),
-          _vec("row_of", row_of, torch.int32, (T * k,)), _vec("topk_w", topk_w, f, (T, k)), T,
-          _vec("dy", dy, bf, (T * k, H)), _vec("dtopk_w", dtopk_w, f, (T, k)))
+    dev, _, shape = _matrix("dout", dout)
+    T, k, H = shape[0], c.num_experts_per_tok, c.hidden
+    _call(lib().moe_combine_backward, "moe_combine_backward", dev, stream, c,
+          _vec("dout", dout, dev, h, (T, H)), _vec("y", y, dev, h, (T * k, H)),
+          _vec("row_of", row_of, dev, i, (T * k,)), _vec("topk_w", topk_w, dev, f, (T, k)), T,
+          _vec("dy", dy, dev, h, (T * k, H)), _vec("dtopk_w", dtopk_w, dev, f, (T, k)))
 
 
 def moe_linear(x, w, bias, residual, y, pre=None, act="none", dev_status=None, stream=None):
     """y [M, N] = act(x [M, K] w [N, K]^T + bias) + residual, bf16 or f16; bias fp32 [N] or None,
     residual [M, N] or None, pre [M, N] (None: not wanted) receives the value before act. Rows of
     x and w start on 16-byte boundaries (strides in multiples of 8 elements)."""
-    import torch
-    M, N, K = x.shape[0], w.shape[0], x.shape[1]
-    px, ldx = _rows("x", x)
-    pw, ldw = _rows("w", w, x.dtype, (N, K))
-    py, ldy = _rows("y", y, x.dtype, (M, N))
-    pr, ldr = _rows("residual", residual, x.dtype, (M, N)) if residual is not None else (None, N)
-    pp, ldp = _rows("pre", pre, x.dtype, (M, N)) if pre is not None else (None, N)
-    _call(lib().moe_linear, "moe_linear", (x, w, bias, residual, y, pre, dev_status), stream,
-          _dtype("x", x), px, ldx, pw, ldw, _vec("bias", bias, torch.float32, (N,)), pr, ldr, ACT[act], M,
-          N, K, py, ldy, pp, ldp, _vec("dev_status", dev_status, torch.int32, (1,)))
+    from torch import float32 as f, int32 as i
+    dev, dt, shape = _matrix("x", x)
+    M, K = shape
+    N, t = w.shape[0], x.dtype
+    px, ldx = _rows("x", x, dev, t, shape)
+    pw, ldw = _rows("w", w, dev, t, (N, K))
+    py, ldy = _rows("y", y, dev, t, (M, N))
+    pr, ldr = _rows("residual", residual, dev, t, (M, N)) if residual is not None else (None, N)
+    pp, ldp = _rows("pre", pre, dev, t, (M, N)) if pre is not None else (None, N)
+    _call(lib().moe_linear, "moe_linear", dev, stream, dt, px, ldx, pw, ldw,
+          _vec("bias", bias, dev, f, (N,)), pr, ldr, ACT[act], M, N, K, py, ldy, pp, ldp,
+          _vec("dev_status", dev_status, dev, i, (1,)))
 
 
 def moe_linear_backward_workspace_bytes(M: int, N: int, K: int, act="none") -> int:
@@ -472,19 +502,20 @@ def moe_linear_backward(dy, x, w, pre, dx, dw, db, ws, act="none", dev_status=No
     """Gradients of moe_linear: dx like x, dw like w, db fp32 [N]; each may be None. pre as
     moe_linear wrote it (None for act="none"); the residual's gradient is dy. ws: at least
     moe_linear_backward_workspace_bytes(M, N, K, act) bytes."""
-    import torch
-    M, N, K = x.shape[0], w.shape[0], x.shape[1]
-    px, ldx = _rows("x", x)
-    pw, ldw = _rows("w", w, x.dtype, (N, K))
-    pg, ldg = _rows("dy", dy, x.dtype, (M, N))
-    pp, ldp = _rows("pre", pre, x.dtype, (M, N)) if pre is not None else (None, N)
-    pdx, lddx = _rows("dx", dx, x.dtype, (M, K)) if dx is not None else (None, K)
-    pdw, lddw = _rows("dw", dw, x.dtype, (N, K)) if dw is not None else (None, K)
-    _call(lib().moe_linear_backward, "moe_linear_backward", (x, dy, w, pre, dx, dw, db, ws, dev_status),
-          stream, _dtype("x", x), pg, ldg, px, ldx, pw, ldw, pp, ldp, ACT[act], M, N, K, pdx, lddx, pdw,
-          lddw, _vec("db", db, torch.float32, (N,)), _ptr(ws),
-          0 if ws is None else ws.numel() * ws.element_size(),
-          _vec("dev_status", dev_status, torch.int32, (1,)))
+    from torch import float32 as f, int32 as i
+    dev, dt, shape = _matrix("x", x)
+    M, K = shape
+    N, t = w.shape[0], x.dtype
+    px, ldx = _rows("x", x, dev, t, shape)
+    pw, ldw = _rows("w", w, dev, t, (N, K))
+    pg, ldg = _rows("dy", dy, dev, t, (M, N))
+    pp, ldp = _rows("pre", pre, dev, t, (M, N)) if pre is not None else (None, N)
+    pdx, lddx = _rows("dx", dx, dev, t, shape) if dx is not None else (None, K)
+    pdw, lddw = _rows("dw", dw, dev, t, (N, K)) if dw is not None else (None, K)
+    pws, nws = _bytes("ws", ws, dev)
+    _call(lib().moe_linear_backward, "moe_linear_backward", dev, stream, dt, pg, ldg, px, ldx, pw, ldw, pp,
+          ldp, ACT[act], M, N, K, pdx, lddx, pdw, lddw, _vec("db", db, dev, f, (N,)), pws, nws,
+          _vec("dev_status", dev_status, dev, i, (1,)))
 
 
 class MoELayer:

@@ -41,6 +41,86 @@ struct alignas(sizeof(T) * VEC) Pack {
 template <typename T>
 constexpr int kFullVec = 16 / (int)sizeof(T);
 
+// Two fp32 values in a 64-bit register pair, and the packed operations on them (one
+// instruction for both).
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum2(f32x2 v) {
+    const float2 f = unpack2(v);
+    return f.x + f.y;
+}
+
+// 16 bytes of T as pairs of fp32, and back (one rounding).
+template <typename T>
+constexpr int kPairs = 8 / (int)sizeof(T);
+
+template <typename T>
+__device__ __forceinline__ void widen(const uint4& u, f32x2 (&v)[kPairs<T>]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (sizeof(T) == 4) {
+        v[0] = pack2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        v[1] = pack2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (is_half<T>()) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                v[i] = pack2(f.x, f.y);
+            } else {
+                v[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            }
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 narrow(const f32x2 (&v)[kPairs<T>]) {
+    uint32_t w[4];
+    if constexpr (sizeof(T) == 4) {
+        const float2 a = unpack2(v[0]), b = unpack2(v[1]);
+        w[0] = __float_as_uint(a.x); w[1] = __float_as_uint(a.y);
+        w[2] = __float_as_uint(b.x); w[3] = __float_as_uint(b.y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2(v[i]);
+            if constexpr (is_half<T>()) {
+                const __half2 h = __floats2half2_rn(f.x, f.y);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 inline int esize(int dtype) { return dtype == MOE_T_F32 ? 4 : 2; }
 
 }  // namespace moe

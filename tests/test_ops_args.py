@@ -129,22 +129,24 @@ def test_binding_refuses_before_the_library(lib):
         moe.moe_route(W.CONFIGS["tiny_bf16"], torch.zeros(4, 16), None, None, None)
     with pytest.raises(ValueError, match="not on a CUDA device"):
         moe.moe_combine_backward(W.CONFIGS["tiny_bf16"], torch.zeros(4, 256), None, None, None, None, None)
-    with pytest.raises(ValueError, match="is missing"):
-        moe._rows("x", None)
 
 
 class _Fake:
     """Stands for a device tensor in the binding's checks."""
     is_cuda = True
+    device = "cuda:0"
 
-    def __init__(self, shape, stride, dtype=torch.bfloat16):
-        self.shape, self._s, self.dtype = shape, stride, dtype
+    def __init__(self, shape, stride, dtype=torch.bfloat16, dev=0):
+        self.shape, self._s, self.dtype, self._d = shape, stride, dtype, dev
 
     def dim(self):
         return len(self.shape)
 
-    def stride(self, i):
-        return self._s[i]
+    def stride(self):
+        return self._s
+
+    def get_device(self):
+        return self._d
 
     def is_contiguous(self):
         return False
@@ -154,15 +156,25 @@ class _Fake:
 
 
 def test_binding_checks_layout():
-    assert moe._rows("x", _Fake((4, 64), (72, 1))) == (4096, 72)
-    assert moe._rows("x", _Fake((1, 64), (1, 1))) == (4096, 64)
-    for shape, stride, why in [((4, 64), (64, 2), "adjacent"), ((4, 64), (32, 1), "overlap"),
-                               ((64,), (1,), "shape"), ((4, 64), (0, 1), "overlap")]:
+    bf = torch.bfloat16
+    rows = lambda t, shape=(4, 64), dtype=bf: moe._rows("x", t, 0, dtype, shape)
+    assert rows(_Fake((4, 64), (72, 1))) == (4096, 72)
+    assert rows(_Fake((1, 64), (1, 1)), (1, 64)) == (4096, 64)
+    for t, why in [(_Fake((4, 64), (64, 2)), "adjacent"), (_Fake((4, 64), (32, 1)), "overlap"),
+                   (_Fake((4, 64), (0, 1)), "overlap"), (_Fake((4, 65), (65, 1)), "shape"),
+                   (_Fake((64,), (1,)), "shape"), (None, "is missing"),
+                   (_Fake((4, 64), (64, 1), dev=1), "not on CUDA device 0"),
+                   (_Fake((4, 64), (64, 1), torch.float16), "not torch.bfloat16")]:
         with pytest.raises(ValueError, match=why):
-            moe._rows("x", _Fake(shape, stride))
+            rows(t)
     with pytest.raises(ValueError, match="contiguous"):
-        moe._vec("w", _Fake((64,), (2,)), torch.bfloat16, (64,))
+        moe._vec("w", _Fake((64,), (2,)), 0, bf, (64,))
     with pytest.raises(ValueError, match="not torch.float32"):
-        moe._vec("w", _Fake((64,), (1,)), torch.float32, (64,))
+        moe._vec("w", _Fake((64,), (1,)), 0, torch.float32, (64,))
+    with pytest.raises(ValueError, match="contiguous"):
+        moe._bytes("ws", _Fake((64,), (2,)), 0)
+    assert moe._bytes("ws", None, 0) == (None, 0)
     with pytest.raises(ValueError, match="float32 is wanted"):
-        moe._dtype("x", _Fake((4, 64), (64, 1), torch.float64))
+        moe._matrix("x", _Fake((4, 64), (64, 1), torch.float64))
+    with pytest.raises(ValueError, match="a matrix"):
+        moe._matrix("x", _Fake((64,), (1,)))
