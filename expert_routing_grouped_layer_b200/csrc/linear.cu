@@ -22,6 +22,8 @@
 //                        equal bits.
 // Sums are fp32 in tensor memory; y, pre, dx and dW are rounded once to the tensors'
 // type, and g once between dy and the products (the tensor cores take 16-bit operands).
+#include <type_traits>
+
 #include "gemm_common.cuh"
 #include "types.cuh"
 
@@ -49,8 +51,27 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t smem_addr) {
 }
 
 template <bool MN>
-__device__ __forceinline__ uint64_t sdesc(uint32_t base, int kk) {
-    return MN ? sdesc_mnmajor_sw128(base + kk * 2048) : sdesc_kmajor_sw128(base + kk * 32);
+__device__ __forceinline__ uint64_t sdesc(uint32_t base) {
+    return MN ? sdesc_mnmajor_sw128(base) : sdesc_kmajor_sw128(base);
+}
+// Descriptor step (16-byte units, the descriptor's low field) of one MMA's 16 k.
+template <bool MN>
+constexpr uint64_t kStep = MN ? 2048 / 16 : 32 / 16;
+
+// The MMA loops run on whole warps, and one lane issues: with the loop's state uniform over
+// the warp the descriptors stay in uniform registers and advance by additions. (Issued
+// from one lane's own loop, which rebuilt them, four MMAs took 540 cycles however narrow
+// the tile.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+// mbar_wait by a converged warp, the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 
 // Instruction descriptor, kind::f16: fp32 accumulator, A and B both bf16 or both f16,
@@ -80,7 +101,7 @@ struct Epilogue {
     void* pre;  // or null
     long ld_res, ld_out, ld_pre;
     int rows, cols, act;
-    int vec;  // out, res and pre allow 4-element accesses
+    int vec;  // out, res, pre and bias allow 4-element accesses
 };
 
 constexpr float kSqrtHalf = 0.70710678118654752f;
@@ -88,16 +109,36 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kSqrt2OverPi = 0.79788456080286536f;
 constexpr float kGeluCubic = 0.044715f;
 
-__device__ __forceinline__ float sigmoid_f(float z) { return 1.0f / (1.0f + __expf(-z)); }
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
 // tanh through one exponential: accurate to a few units of 2^-24 of 1, saturating cleanly
 __device__ __forceinline__ float tanh_f(float u) { return 1.0f - __fdividef(2.0f, 1.0f + __expf(2.0f * u)); }
 
-__device__ __forceinline__ float act_f(float z, int act) {
-    switch (act) {
+// The normal distribution's Phi(z) and exp(-z^2 / 2) by Abramowitz and Stegun's 7.1.26 (erfc
+// as a polynomial in 1 / (1 + 0.3275911 x) times exp(-x^2), |error| <= 1.5e-7): no
+// branch, two special-function operations. erff's two ranges diverge within a warp; with
+// it the GELU epilogue took 11.6 us a tile.
+__device__ __forceinline__ float normal_cdf(float z, float& gauss) {
+    const float x = fabsf(z) * kSqrtHalf;
+    gauss = __expf(-x * x);
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    float p = fmaf(t, 1.061405429f, -1.453152027f);
+    p = fmaf(t, p, 1.421413741f);
+    p = fmaf(t, p, -0.284496736f);
+    p = fmaf(t, p, 0.254829592f);
+    const float tail = 0.5f * p * t * gauss;  // Phi(-|z|)
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_f(float z) {
+    switch (ACT) {
     case MOE_ACT_RELU: return z < 0.0f ? 0.0f : z;  // NaN stays NaN
     case MOE_ACT_SILU: return z * sigmoid_f(z);
-    case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    case MOE_ACT_GELU: {
+        float gauss;
+        return z * normal_cdf(z, gauss);
+    }
     case MOE_ACT_GELU_TANH:
         return 0.5f * z * (1.0f + tanh_f(kSqrt2OverPi * (z + kGeluCubic * z * z * z)));
     }
@@ -111,8 +152,11 @@ __device__ __forceinline__ float act_slope(float z, int act) {
         const float s = sigmoid_f(z);
         return s * (1.0f + z * (1.0f - s));
     }
-    case MOE_ACT_GELU:
-        return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
+    case MOE_ACT_GELU: {
+        float gauss;
+        const float cdf = normal_cdf(z, gauss);
+        return fmaf(z * kInvSqrt2Pi, gauss, cdf);
+    }
     case MOE_ACT_GELU_TANH: {
         const float t = tanh_f(kSqrt2OverPi * (z + kGeluCubic * z * z * z));
         return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * kSqrt2OverPi * (1.0f + 3.0f * kGeluCubic * z * z);
@@ -121,40 +165,60 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     return 1.0f;
 }
 
-// Bias of columns col..col+3 (zero outside).
-__device__ __forceinline__ void bias4(const Epilogue& e, int col, float (&b)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = e.bias && col + j < e.cols ? e.bias[col + j] : 0.f;
+// Calls f with the activation as a compile-time constant: one branch for a group of values.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+    switch (act) {
+    case MOE_ACT_RELU: f(std::integral_constant<int, MOE_ACT_RELU>()); break;
+    case MOE_ACT_SILU: f(std::integral_constant<int, MOE_ACT_SILU>()); break;
+    case MOE_ACT_GELU: f(std::integral_constant<int, MOE_ACT_GELU>()); break;
+    case MOE_ACT_GELU_TANH: f(std::integral_constant<int, MOE_ACT_GELU_TANH>()); break;
+    default: f(std::integral_constant<int, MOE_ACT_NONE>());
+    }
 }
 
-// Four neighbouring results of one row: bias, pre, activation, residual, store.
+// Bias of columns col..col+3 (zero outside).
+__device__ __forceinline__ float4 bias4(const Epilogue& e, int col) {
+    float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!e.bias) return b;
+    if (e.vec && col + 4 <= e.cols) return *reinterpret_cast<const float4*>(e.bias + col);
+    if (col < e.cols) b.x = e.bias[col];
+    if (col + 1 < e.cols) b.y = e.bias[col + 1];
+    if (col + 2 < e.cols) b.z = e.bias[col + 2];
+    if (col + 3 < e.cols) b.w = e.bias[col + 3];
+    return b;
+}
+
+// Whether columns col..col+3 move by one access.
+__device__ __forceinline__ bool quad_at(const Epilogue& e, int col) { return e.vec && col + 4 <= e.cols; }
+
+// Residual of four neighbouring elements, raw, loaded ahead of its use where quad_at. (As
+// separate 16-bit values the load would be unpacked, and so waited for, on the spot.)
 template <typename T>
-__device__ __forceinline__ void store4(const Epilogue& e, const float (&acc)[4], const float (&b)[4],
-                                       long row, int col) {
-    float z[4], y[4];
+__device__ __forceinline__ uint2 res4(const Epilogue& e, long row, int col) {
+    return *reinterpret_cast<const uint2*>(static_cast<const T*>(e.res) + row * e.ld_res + col);
+}
+
+// Four neighbouring results of one row: bias, pre, activation, residual, store. r: the
+// residual where quad_at, else it is read here.
+template <typename T, int ACT>
+__device__ __forceinline__ void store4(const Epilogue& e, float4 acc, float4 b, uint2 r, long row, int col) {
+    const float z[4] = {acc.x + b.x, acc.y + b.y, acc.z + b.z, acc.w + b.w};
+    float y[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) z[j] = acc[j] + b[j];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = act_f(z[j], e.act);
+    for (int j = 0; j < 4; ++j) y[j] = act_f<ACT>(z[j]);
     T* out = static_cast<T*>(e.out) + row * e.ld_out + col;
     T* pre = static_cast<T*>(e.pre) + row * e.ld_pre + col;
-    const T* res = static_cast<const T*>(e.res) + row * e.ld_res + col;
-    if (e.vec && col + 4 <= e.cols) {
-        Pack<T, 4> o;
-        if (e.pre) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o.v[j] = from_f32<T>(z[j]);
-            *reinterpret_cast<Pack<T, 4>*>(pre) = o;
-        }
+    if (quad_at(e, col)) {
+        if (e.pre) *reinterpret_cast<uint2*>(pre) = narrow4<T>(z);
         if (e.res) {
-            const Pack<T, 4> r = *reinterpret_cast<const Pack<T, 4>*>(res);
+            const Pack<T, 4> p = *reinterpret_cast<const Pack<T, 4>*>(&r);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] += to_f32<T>(r.v[j]);
+            for (int j = 0; j < 4; ++j) y[j] += to_f32<T>(p.v[j]);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o.v[j] = from_f32<T>(y[j]);
-        *reinterpret_cast<Pack<T, 4>*>(out) = o;
+        *reinterpret_cast<uint2*>(out) = narrow4<T>(y);
     } else {
+        const T* res = static_cast<const T*>(e.res) + row * e.ld_res + col;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (col + j >= e.cols) break;
@@ -174,17 +238,21 @@ struct GemmDims {
 // 256 rows x BN columns per pair: each SM loads its 128 rows and half of the columns'
 // operand, and drains its own 128 accumulator rows.
 //   warp 0  TMA, warp 1 MMA (leader), warps 2-9 epilogue: four lane quadrants x two
-//   groups that take alternate 32-column chunks. A chunk goes through the warp's own
-//   4 KB of shared memory (16-byte pieces swizzled by row), so that global accesses run
-//   along rows: 8 lanes per 64-byte row piece.
+//   groups that take alternate 32-column chunks.
+// Epilogue with outputs on the 16-byte grid (TMA_OUT): a lane finishes one row's 32 columns
+// in registers, the warp's 32 x 32 block goes through 2 KB of swizzled shared memory and
+// leaves (and the residual comes) by TMA, which also clips it to the matrix. Otherwise a
+// chunk goes through shared memory as fp32 and lanes store along rows, element by element
+// where need be; with the residual that took 13.8 us a tile against the main loop's 14.5 us
+// at K = 2048 and held the tensor cores up.
 struct PairCfg {
     static constexpr int A_BYTES = 128 * BK * 2;
-    static constexpr int STAGE_BYTES = 2 * A_BYTES;  // and up to 128 columns of the other
-    static constexpr int STAGES = 6;
+    static constexpr int RING_BYTES = 6 * 2 * A_BYTES;  // six stages of a 256-column tile, more of a narrower one
+    static constexpr int MAX_STAGES = 9;
     static constexpr int EPI_WARPS = 8;
     static constexpr int EPI_BYTES = EPI_WARPS * 4096;
     static constexpr int THREADS = 32 * (2 + EPI_WARPS);
-    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + 8 * (2 * STAGES + 5) + 16;
+    static constexpr int SMEM_BYTES = 1024 + RING_BYTES + EPI_BYTES + 8 * (2 * MAX_STAGES + 5 + 2 * EPI_WARPS) + 16;
     static_assert(SMEM_BYTES <= kSmemMax, "shared memory budget");
 };
 
@@ -198,23 +266,44 @@ __device__ __forceinline__ void tile_of(int u, int mt, int nt, int& tm, int& tn)
     tm = b * 8 + (r - tn * h);
 }
 
-template <typename T, bool A_MN, bool B_MN>
+__device__ __forceinline__ void tma_store_2d(const void* tmap, const void* smem_src, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(smem_u32(smem_src)), "r"(x), "r"(y)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Tensor maps of the epilogue's matrices, boxes of 32 x 32 elements, 64-byte swizzle.
+struct OutMaps {
+    CUtensorMap out, pre, res;
+};
+
+template <typename T, bool A_MN, bool B_MN, bool TMA_OUT>
 __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const GemmDims d, const Epilogue epi, const int BN) {
+                       const __grid_constant__ OutMaps tmO, const GemmDims d, const Epilogue epi, const int BN) {
     pdl_wait();
     pdl_trigger();
     using C = PairCfg;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t* stage_out = smem + C::STAGES * C::STAGE_BYTES;
+    uint8_t* stage_out = smem + C::RING_BYTES;
     uint64_t* full = reinterpret_cast<uint64_t*>(stage_out + C::EPI_BYTES);
-    uint64_t* empty = full + C::STAGES;
-    uint64_t* tfull = empty + C::STAGES;
+    uint64_t* empty = full + C::MAX_STAGES;
+    uint64_t* tfull = empty + C::MAX_STAGES;
+    const int half = BN / 2;
+    const int b_boxes = B_MN ? (half + 63) / 64 : 1;
+    const int stage_bytes = C::A_BYTES + (B_MN ? b_boxes * 8192 : half * BK * 2);
+    const int stages = min(C::MAX_STAGES, C::RING_BYTES / stage_bytes);
     uint64_t* tempty = tfull + 2;
     uint64_t* mma_done = tempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    uint64_t* res_full = mma_done + 1;  // two per epilogue warp: a residual block is in
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + 2 * C::EPI_WARPS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5;
@@ -223,7 +312,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(&full[s], 1);   // the leader's expect-tx arrival covers both SMs' copies
             mbar_init(&empty[s], 1);  // the leader's multicast commit
         }
@@ -232,6 +321,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
             mbar_init(&tempty[a], 2 * C::EPI_WARPS);  // both SMs' epilogue warps (leader's copy used)
         }
         mbar_init(mma_done, 1);
+        for (int w = 0; w < 2 * C::EPI_WARPS; ++w) mbar_init(&res_full[w], 1);
         *abort_flag = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tmA);
@@ -248,15 +338,13 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
     const int mt = (d.R + 255) / 256, nt = (d.C + BN - 1) / BN, total = mt * nt;
     const int KB = (d.K + BK - 1) / BK;
-    const int half = BN / 2;
 
     if (warp == 0) {
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
             int issued = 0;
-            const int b_boxes = B_MN ? (half + 63) / 64 : 1;
-            const uint32_t tx = 2u * (uint32_t)(C::A_BYTES + (B_MN ? b_boxes * 8192 : half * BK * 2));
+            const uint32_t tx = 2u * (uint32_t)stage_bytes;
             for (int u = pair; u < total && !*abort_flag; u += npairs) {
                 int tm, tn;
                 tile_of(u, mt, nt, tm, tn);
@@ -264,7 +352,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                 bool ok = true;
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-                    uint8_t* st = smem + stage * C::STAGE_BYTES;
+                    uint8_t* st = smem + stage * stage_bytes;
                     const uint32_t lfull = peer_addr(&full[stage], 0);
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], tx);
                     if (A_MN) {
@@ -281,7 +369,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                         tma_load_2d_pair(sb, &tmB, kb * BK, rb, lfull);
                     }
                     ++issued;
-                    if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+                    if (++stage == stages) { stage = 0; phase ^= 1; }
                 }
                 if (!ok) break;
             }
@@ -291,8 +379,8 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                     volatile int no_abort = 0;
                     int s = stage;
                     uint32_t ph = phase;
-                    for (int i = 0; i < min(issued, C::STAGES); ++i) {
-                        if (--s < 0) { s = C::STAGES - 1; ph ^= 1; }
+                    for (int i = 0; i < min(issued, stages); ++i) {
+                        if (--s < 0) { s = stages - 1; ph ^= 1; }
                         mbar_wait(&full[s], ph, &no_abort);
                     }
                 }
@@ -300,85 +388,261 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             int stage = 0;
             uint32_t phase = 0;
             int acc = 0;
             uint32_t acc_phase = 0;
             const uint32_t idesc = idesc_16<T, A_MN, B_MN>(256, BN);
+            const uint64_t da = sdesc<A_MN>(smem_u32(smem)), db = sdesc<B_MN>(smem_u32(smem) + C::A_BYTES);
             for (int u = pair; u < total; u += npairs) {
-                if (!mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag)) break;
+                if (!warp_wait(&tempty[acc], acc_phase ^ 1, abort_flag)) break;
                 tc_fence_after();
                 const uint32_t d0 = tmem_base + acc * 256;
                 bool ok = true;
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+                    if (!warp_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + stage * C::STAGE_BYTES);
-                    const uint32_t sb = sa + C::A_BYTES;
+                    const uint64_t off = (uint64_t)((uint32_t)(stage * stage_bytes) >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk)
-                        mma_pair_f16(d0, sdesc<A_MN>(sa, kk), sdesc<B_MN>(sb, kk), idesc, (kb | kk) != 0);
-                    mma_commit_pair(&empty[stage]);
-                    if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            mma_pair_f16(d0, da + off + kk * kStep<A_MN>, db + off + kk * kStep<B_MN>, idesc,
+                                         (kb | kk) != 0);
+                        mma_commit_pair(&empty[stage]);
+                    }
+                    __syncwarp();
+                    if (++stage == stages) { stage = 0; phase ^= 1; }
                 }
                 if (!ok) break;
-                mma_commit_pair(&tfull[acc]);
+                if (elect_one()) mma_commit_pair(&tfull[acc]);
+                __syncwarp();
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1;
             }
-            mma_commit(mma_done);
-            volatile int no_abort = 0;
-            mbar_wait(mma_done, 0, &no_abort);
-            if (*abort_flag) status_or(d.status, MOE_DEV_TIMEOUT);
+            if (elect_one()) {
+                mma_commit(mma_done);
+                volatile int no_abort = 0;
+                mbar_wait(mma_done, 0, &no_abort);
+                if (*abort_flag) status_or(d.status, MOE_DEV_TIMEOUT);
+            }
+            __syncwarp();
         }
     } else {
         const int q = warp & 3, grp = (warp - 2) >> 2;
-        uint8_t* buf = stage_out + (warp - 2) * 4096;
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        for (int u = pair; u < total; u += npairs) {
-            int tm, tn;
-            tile_of(u, mt, nt, tm, tn);
-            if (!mbar_wait(&tfull[acc], acc_phase, abort_flag)) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
-            const int row0 = tm * 256 + (int)rank * 128 + q * 32;
-            const int chunks = (min(BN, d.C - tn * BN) + 31) / 32;
-            for (int c = grp; c < chunks; c += 2) {
-                uint32_t r0[16], r1[16];
-                tmem_ld16(taddr + c * 32, r0);
-                tmem_ld16(taddr + c * 32 + 16, r1);
-                tmem_ld_wait(r0, r1);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t* s = j < 4 ? &r0[4 * j] : &r1[4 * (j - 4)];
-                    *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                        make_uint4(s[0], s[1], s[2], s[3]);
+        if constexpr (TMA_OUT) {
+            // Buffers of 2 KB: with `pre`, 0 for the result (and residual) and 1 for pre; without,
+            // both alternate for the result, and the next chunk's residual is fetched into the
+            // other one while a chunk is worked on.
+            uint8_t* bufs = stage_out + (warp - 2) * 4096;
+            uint64_t* res_bar = &res_full[2 * (warp - 2)];  // of buffer 0 and 1
+            const bool has_pre = epi.pre != nullptr, has_res = epi.res != nullptr;
+            const int y0 = (int)rank * 128 + q * 32;
+            int acc = 0, n = 0;  // n: chunks this warp has worked on
+            uint32_t acc_phase = 0;
+            auto fetch = [&](int u, int c, int to) {  // lane 0: residual of chunk c of tile u
+                int tm, tn;
+                tile_of(u, mt, nt, tm, tn);
+                mbar_arrive_expect_tx(&res_bar[to], 2048);
+                tma_load_2d(bufs + to * 2048, &tmO.res, tn * BN + c * 32, tm * 256 + y0, &res_bar[to]);
+            };
+            auto chunks_of = [&](int u) {
+                int tm, tn;
+                tile_of(u, mt, nt, tm, tn);
+                return (min(BN, d.C - tn * BN) + 31) / 32;
+            };
+            // the chunk of this warp after chunk c of tile u (u >= total: none)
+            auto advance = [&](int& u, int& c) {
+                c += 2;
+                while (u < total && c >= chunks_of(u)) {
+                    u += npairs;
+                    c = grp;
                 }
-                __syncwarp();
-                const int piece = lane & 7, col = tn * BN + c * 32 + piece * 4;
-                float b[4];
-                bias4(epi, col, b);
-                if (col < d.C) {
+            };
+            int nu = pair, nc = grp - 2;
+            advance(nu, nc);  // the first chunk
+            const bool early = has_res && !has_pre;
+            int fetched = 0;
+            if (early && lane == 0 && nu < total) {
+                fetch(nu, nc, 0);
+                ++fetched;
+            }
+            bool ok = true;
+            for (int u = pair; u < total && ok; u += npairs) {
+                int tm, tn;
+                tile_of(u, mt, nt, tm, tn);
+                if (!mbar_wait(&tfull[acc], acc_phase, abort_flag)) break;
+                tc_fence_after();
+                const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
+                const int chunks = chunks_of(u);
+                const int row = tm * 256 + y0;
+                for (int c = grp; c < chunks; c += 2, ++n) {
+                    const int col = tn * BN + c * 32;
+                    const int bi = has_pre ? 0 : n & 1;
+                    uint8_t* buf = bufs + bi * 2048;
+                    if (has_pre && lane == 0) {
+                        bulk_wait_read<0>();  // the last chunk's blocks have left
+                        if (has_res) {
+                            fetch(u, c, 0);
+                            ++fetched;
+                        }
+                    }
+                    uint32_t r0[16], r1[16];
+                    tmem_ld16(taddr + c * 32, r0);
+                    tmem_ld16(taddr + c * 32 + 16, r1);
+                    float z[32];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = i * 4 + (lane >> 3);
-                        const float4 v = *reinterpret_cast<const float4*>(buf + r * 128 + ((piece ^ (r & 7)) << 4));
-                        const float a[4] = {v.x, v.y, v.z, v.w};
-                        if (row0 + r < d.R) store4<T>(epi, a, b, row0 + r, col);
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 b = bias4(epi, col + 4 * j);
+                        z[4 * j] = b.x; z[4 * j + 1] = b.y; z[4 * j + 2] = b.z; z[4 * j + 3] = b.w;
+                    }
+                    tmem_ld_wait(r0, r1);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        z[j] += __uint_as_float(r0[j]);
+                        z[j + 16] += __uint_as_float(r1[j]);
+                    }
+                    if (!has_pre && lane == 0) {
+                        if (early) {
+                            bulk_wait_read<0>();  // the other buffer is free
+                            advance(nu, nc);
+                            if (nu < total) {
+                                fetch(nu, nc, bi ^ 1);
+                                ++fetched;
+                            }
+                        } else {
+                            bulk_wait_read<1>();  // this buffer is free
+                        }
+                    }
+                    __syncwarp();
+                    uint8_t* mine = buf + lane * 64;
+                    const int swz = (lane >> 1) & 3;
+                    if (has_pre) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4*>(mine + 2048 + ((j ^ swz) << 4)) = narrow8<T>(&z[8 * j]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && row < d.R) tma_store_2d(&tmO.pre, bufs + 2048, col, row);
+                    }
+                    with_act(epi.act, [&](auto act) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) z[j] = act_f<act.value>(z[j]);
+                    });
+                    if (has_res) {
+                        // every lane waits itself (that makes the block visible to it)
+                        const uint32_t parity = (uint32_t)(has_pre ? n : n >> 1) & 1u;
+                        ok = __all_sync(0xffffffffu, mbar_wait(&res_bar[bi], parity, abort_flag));
+                        if (!ok) break;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint4 r = *reinterpret_cast<const uint4*>(mine + ((j ^ swz) << 4));
+                            f32x2 f[4];
+                            widen<T>(r, f);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 g = unpack2(f[i]);
+                                z[8 * j + 2 * i] += g.x;
+                                z[8 * j + 2 * i + 1] += g.y;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint4*>(mine + ((j ^ swz) << 4)) = narrow8<T>(&z[8 * j]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (row < d.R) tma_store_2d(&tmO.out, buf, col, row);
+                        bulk_commit();
                     }
                 }
+                tc_fence_before();
                 __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(&tempty[acc]);
+                    else mbar_arrive_remote(peer_addr(&tempty[acc], 0));
+                }
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1;
             }
-            tc_fence_before();
-            __syncwarp();
             if (lane == 0) {
-                if (rank == 0) mbar_arrive(&tempty[acc]);
-                else mbar_arrive_remote(peer_addr(&tempty[acc], 0));
+                // blocks still on their way (only after a wait ran out) land before the CTA exits
+                if (*abort_flag) {
+                    volatile int no_abort = 0;
+                    for (int f = max(0, fetched - 2); f < fetched; ++f)
+                        mbar_wait(&res_bar[has_pre ? 0 : f & 1], (uint32_t)(has_pre ? f : f >> 1) & 1u, &no_abort);
+                    status_or(d.status, MOE_DEV_TIMEOUT);
+                }
+                bulk_wait_all();
             }
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1;
+        } else {
+            const int piece = lane & 7, sub = lane >> 3;  // columns 4 piece.., rows sub, sub + 4, ...
+            uint8_t* buf = stage_out + (warp - 2) * 4096;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            for (int u = pair; u < total; u += npairs) {
+                int tm, tn;
+                tile_of(u, mt, nt, tm, tn);
+                const int row0 = tm * 256 + (int)rank * 128 + q * 32;
+                const int chunks = (min(BN, d.C - tn * BN) + 31) / 32;
+                // bias and residual of a chunk are loaded one chunk ahead, the first before the
+                // accumulator is ready: their latency would otherwise stand in every chunk
+                uint2 res[8];
+                float4 b;
+                auto ahead = [&](int c) {
+                    const int col = tn * BN + c * 32 + piece * 4;
+                    b = bias4(epi, col);
+                    if (epi.res && quad_at(epi, col)) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (row0 + i * 4 + sub < d.R) res[i] = res4<T>(epi, row0 + i * 4 + sub, col);
+                    }
+                };
+                ahead(grp);
+                if (!mbar_wait(&tfull[acc], acc_phase, abort_flag)) break;
+                tc_fence_after();
+                const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
+                for (int c = grp; c < chunks; c += 2) {
+                    uint32_t r0[16], r1[16];
+                    tmem_ld16(taddr + c * 32, r0);
+                    tmem_ld16(taddr + c * 32 + 16, r1);
+                    tmem_ld_wait(r0, r1);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t* s = j < 4 ? &r0[4 * j] : &r1[4 * (j - 4)];
+                        *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                            make_uint4(s[0], s[1], s[2], s[3]);
+                    }
+                    __syncwarp();
+                    const int col = tn * BN + c * 32 + piece * 4;
+                    const float4 bc = b;
+                    uint2 rc[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) rc[i] = res[i];
+                    if (c + 2 < chunks) ahead(c + 2);
+                    if (col < d.C) {
+                        with_act(epi.act, [&](auto act) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int r = i * 4 + sub;
+                                const float4 v =
+                                    *reinterpret_cast<const float4*>(buf + r * 128 + ((piece ^ (r & 7)) << 4));
+                                if (row0 + r < d.R) store4<T, act.value>(epi, v, bc, rc[i], row0 + r, col);
+                            }
+                        });
+                    }
+                    __syncwarp();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(&tempty[acc]);
+                    else mbar_arrive_remote(peer_addr(&tempty[acc], 0));
+                }
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1;
+            }
         }
     }
 
@@ -392,25 +656,36 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
 }
 
 // ------------------------------------------------------------------ split-K clusters
-// One tile per cluster: 128 columns (MMA M, the matrix of the columns) x BT rows (MMA N).
-// Each of the cluster's CTAs runs its share of the k blocks; the partial tiles, [row][128]
-// fp32 in each CTA's shared memory, are added in rank order by the CTA that stores the row.
-constexpr int kSplitThreads = 256;  // warp 0 TMA, warp 1 MMA, warps 4-7 drain, all store
-
-constexpr int kSplitFixed = 1024 + 8 * (2 * 16 + 1) + 32;
+// One tile per cluster: 128 columns (MMA M, the matrix of the columns) x BT <= 128 rows
+// (MMA N). Each of the cluster's CTAs runs its share of the k blocks and leaves its partial
+// tile as [row][128] fp32 in its own shared memory; CTA p gathers rows p RP .. of all the
+// partial tiles by bulk copies between the SMs, which complete on its barrier, adds them in
+// rank order and stores them. (Reading the partial tiles through cluster barriers instead
+// cost two release fences, ~1.5 us each, and the loads' latency once per peer.)
+constexpr int kSplitThreads = 256;  // warp 0 TMA, warp 1 MMA; all drain, add and store
+constexpr int kSplitMaxRows = 128;
+constexpr int kSplitMaxStages = 12;
+constexpr int kSplitHalf = 110 * 1024;  // shared memory of a CTA that shares its SM with another
+constexpr int kSplitFixed = 1024 + 8 * (2 * kSplitMaxStages + 2) + 16;
 
 template <bool MN>
 __host__ __device__ constexpr int row_bytes_of(int bt) {  // shared-memory bytes of the row operand
     return MN ? (bt + 63) / 64 * 8192 : bt * BK * 2;
 }
 
-__device__ __forceinline__ float4 ld_peer(const void* p, uint32_t rank) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(peer_addr(p, rank))
-                 : "memory");
-    return v;
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Bulk copy from this CTA's shared memory into that of cluster CTA `rank`, completing on
+// the barrier at the same offset there.
+__device__ __forceinline__ void copy_to_peer(void* dst, uint64_t* bar, uint32_t rank, const void* src, uint32_t bytes) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            peer_addr(dst, rank)),
+        "r"(smem_u32(src)), "r"(bytes), "r"(peer_addr(bar, rank))
+        : "memory");
 }
 
 template <typename T, bool A_MN, bool B_MN>
@@ -426,11 +701,13 @@ __global__ void __launch_bounds__(kSplitThreads)
     constexpr int A_BYTES = 128 * BK * 2;
     const int b_bytes = row_bytes_of<B_MN>(BT);
     const int stage_bytes = A_BYTES + b_bytes;
-    const int data = max(stages * stage_bytes, BT * 512);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + data);
+    const int RP = (BT + split - 1) / split;  // rows a CTA adds and stores
+    float* gather = reinterpret_cast<float*>(smem + stages * stage_bytes);  // [split][RP][128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(gather + (split > 1 ? split * RP * 128 : 0));
     uint64_t* empty = full + stages;
     uint64_t* tfull = empty + stages;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
+    uint64_t* gathered = tfull + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gathered + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5;
@@ -441,6 +718,8 @@ __global__ void __launch_bounds__(kSplitThreads)
     const int c0 = (tile % ct) * 128, r0 = (tile / ct) * BT;
     const int KB = (d.K + BK - 1) / BK;
     const int kb0 = (int)((long)KB * rank / split), kb1 = (int)((long)KB * (rank + 1) / split);
+    const int n_valid = min(BT, d.R - r0);
+    const int my_rows = max(0, min(RP, n_valid - rank * RP));
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
@@ -448,8 +727,10 @@ __global__ void __launch_bounds__(kSplitThreads)
             mbar_init(&empty[s], 1);
         }
         mbar_init(tfull, 1);
+        mbar_init(gathered, 1);
         *abort_flag = 0;
         fence_barrier_init();
+        if (split > 1 && my_rows > 0) mbar_arrive_expect_tx(gathered, (uint32_t)(split * my_rows * 512));
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
     }
@@ -459,6 +740,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
     tc_fence_before();
     __syncthreads();
+    if (split > 1) cluster_arrive_relaxed();  // the barriers are initialised
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
@@ -498,68 +780,100 @@ __global__ void __launch_bounds__(kSplitThreads)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            const uint32_t idesc = idesc_16<T, A_MN, B_MN>(128, BT);
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(&full[stage], phase, abort_flag)) break;
-                tc_fence_after();
-                const uint32_t sa = smem_u32(smem + stage * stage_bytes);
-                const uint32_t sb = sa + A_BYTES;
+        int stage = 0;
+        uint32_t phase = 0;
+        const uint32_t idesc = idesc_16<T, A_MN, B_MN>(128, BT);
+        const uint64_t da = sdesc<A_MN>(smem_u32(smem)), db = sdesc<B_MN>(smem_u32(smem) + A_BYTES);
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!warp_wait(&full[stage], phase, abort_flag)) break;
+            tc_fence_after();
+            const uint64_t off = (uint64_t)((uint32_t)(stage * stage_bytes) >> 4);
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < BK / 16; ++kk)
-                    mma_bf16(tmem_base, sdesc<A_MN>(sa, kk), sdesc<B_MN>(sb, kk), idesc, kb > kb0 || kk > 0);
+                    mma_bf16(tmem_base, da + off + kk * kStep<A_MN>, db + off + kk * kStep<B_MN>, idesc,
+                             kb > kb0 || kk > 0);
                 mma_commit(&empty[stage]);
-                if (++stage == stages) { stage = 0; phase ^= 1; }
             }
+            __syncwarp();
+            if (++stage == stages) { stage = 0; phase ^= 1; }
+        }
+        if (elect_one()) {
             mma_commit(tfull);
             volatile int no_abort = 0;
             mbar_wait(tfull, 0, &no_abort);  // every MMA this thread issued has finished
             if (*abort_flag) status_or(d.status, MOE_DEV_TIMEOUT);
         }
+        __syncwarp();
     }
     __syncthreads();  // all MMAs are done: the stages are free for the partial tile
     tc_fence_after();
-    const int n_valid = min(BT, d.R - r0);
-    if (warp >= 4) {
+    float* part = reinterpret_cast<float*>(smem);
+    {
         const int q = warp & 3;
-        float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
-        for (int c = 0; c < n_valid; c += 16) {
+        for (int c = (warp >> 2) * 16; c < n_valid; c += 32) {
             uint32_t v[16];
             tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + c, v);
             tmem_ld_wait(v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) part[(c + j) * 128] = __uint_as_float(v[j]);
+            for (int j = 0; j < 16; ++j) part[(c + j) * 128 + q * 32 + lane] = __uint_as_float(v[j]);
         }
     }
     tc_fence_before();
-    if (split > 1) cluster_barrier();
-    else __syncthreads();
     const int col = c0 + lane * 4;
-    float b[4];
-    bias4(epi, col, b);
-    for (int r = rank * 8 + warp; r < n_valid; r += split * 8) {
-        const float* src = reinterpret_cast<const float*>(smem) + r * 128 + lane * 4;
-        float a[4] = {0.f, 0.f, 0.f, 0.f};
-        if (split == 1) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
-            a[0] = v.x; a[1] = v.y; a[2] = v.z; a[3] = v.w;
-        } else {
-#pragma unroll 8
-            for (int p = 0; p < split; ++p) {
-                const float4 v = ld_peer(src, p);
-                a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
+    const float4 b = bias4(epi, col);
+    const float* rows = part;  // of this CTA's first row; partial tiles of the peers RP rows apart
+    bool ok = true;
+    if (split > 1) {
+        fence_proxy_async_smem();
+        __syncthreads();
+        cluster_wait();  // the peers' barriers are initialised
+        if (warp == 0 && lane < split) {
+            const int n = max(0, min(RP, n_valid - lane * RP));
+            if (n > 0)
+                copy_to_peer(gather + rank * RP * 128, gathered, lane, part + lane * RP * 128, (uint32_t)(n * 512));
+        }
+        if (my_rows > 0) ok = mbar_wait(gathered, 0, abort_flag);
+        if (!ok) status_or(d.status, MOE_DEV_TIMEOUT);
+        __syncwarp();
+        cluster_arrive_relaxed();  // the peers' copies to this CTA have landed
+        rows = gather;
+    } else {
+        __syncthreads();
+    }
+    // one row per warp, four at a time, all their loads before the first use
+    constexpr int U = 4;
+    for (int r = warp; r < my_rows && ok; r += 8 * U) {
+        float4 a[U];
+        uint2 res[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int ri = min(r + 8 * i, my_rows - 1);
+            if (epi.res && quad_at(epi, col)) res[i] = res4<T>(epi, r0 + rank * RP + ri, col);
+            a[i] = *reinterpret_cast<const float4*>(rows + ri * 128 + lane * 4);
+        }
+        for (int p = 1; p < split; ++p) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int ri = min(r + 8 * i, my_rows - 1);
+                const float4 v = *reinterpret_cast<const float4*>(rows + (p * RP + ri) * 128 + lane * 4);
+                a[i].x += v.x; a[i].y += v.y; a[i].z += v.z; a[i].w += v.w;
             }
         }
-        if (col < d.C) store4<T>(epi, a, b, r0 + r, col);
+        if (col < d.C)
+            with_act(epi.act, [&](auto act) {
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    if (r + 8 * i < my_rows)
+                        store4<T, act.value>(epi, a[i], b, res[i], r0 + rank * RP + r + 8 * i, col);
+            });
     }
-    if (split > 1) cluster_barrier();  // no CTA leaves while others read its partial tile
-    else __syncthreads();
+    __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, tmem_cols);
     }
+    if (split > 1) cluster_wait();  // every copy out of this CTA has been taken
 }
 
 // ------------------------------------------------------------------ backward, elementwise
@@ -663,14 +977,32 @@ bool operand_map(CUtensorMap* tm, const void* p, long ld, long rows, long K, int
     return make_tmap_2d(tm, kMapType<T>, p, rows, K, ld * 2, BK, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Rows that TMA can address (the stride of a single row counts for nothing).
+inline bool on_grid(const void* p, long ld) {
+    return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0);
+}
+template <typename T>
+bool out_map(CUtensorMap* tm, const void* p, long ld, const GemmDims& d) {
+    return make_tmap_2d(tm, kMapType<T>, p, d.R, d.C, ld * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 // Which kernel and tile: the one whose busiest SM is done first, in SM cycles. A k block
-// of a tile costs its tensor-core time (8192 FLOP a cycle) or its bytes from L2 (about 56 a
+// of a tile costs its tensor-core time (8192 FLOP a cycle) or its bytes from L2 (about 64 a
 // cycle); a tile costs its epilogue besides.
 struct Plan {
     bool pair;
     int bn;                                  // pair: columns per tile
     int bt, split, stages, tmem_cols, smem;  // split
 };
+
+// CTAs of `split`-CTA clusters that fit on the device at once, `per_sm` to an SM. Clusters of
+// 4 and 8 leave SMs over (a GPC's SMs do not divide evenly): on a 148-SM B200 the driver
+// reports 148, 148, 132, 120 CTAs one to an SM, and 296, 296, 284, 264 two to an SM.
+int cluster_capacity(int split, int per_sm) {
+    static const float share[2][4] = {{1.0f, 1.0f, 132.f / 148, 120.f / 148}, {1.0f, 1.0f, 284.f / 296, 264.f / 296}};
+    const int l = split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3;
+    return std::max(split, (int)(per_sm * num_sms() * share[per_sm - 1][l] + 0.5f));
+}
 
 template <bool B_MN>
 Plan plan_gemm(int R, int C, int K) {
@@ -679,31 +1011,39 @@ Plan plan_gemm(int R, int C, int K) {
     double best_t = 1e30;
     for (int bn = 256; bn >= 64; bn -= 32) {
         const long tiles = (long)ceil_div(R, 256) * ceil_div(C, bn);
-        const double kb = std::max(2.0 * bn, (16384 + bn * 64) / 56.0);
+        const double kb = std::max(2.0 * bn, (16384 + bn * 64) / 64.0);
         const double t = ceil_div(tiles, sms / 2) * (KB * kb + 400) + 12.0 * bn + 4000;
         if (t < best_t) {
             best_t = t;
             best = Plan{true, bn};
         }
     }
-    const int passes = ceil_div(R, 256);
+    const int passes = ceil_div(R, kSplitMaxRows);
     const int bt = (ceil_div(R, passes) + 15) / 16 * 16;
     const int stage = 128 * BK * 2 + row_bytes_of<B_MN>(bt);
-    // two CTAs an SM where half the shared memory holds a deep enough ring
-    const int per_sm = 4 * stage <= 110 * 1024 ? 2 : 1;
-    const int budget = per_sm == 2 ? 110 * 1024 : kSmemMax;
-    const int stages = std::min(16, (budget - kSplitFixed) / stage);
-    const long tiles = (long)ceil_div(C, 128) * passes;
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= (long)per_sm * sms && 2 * split * 2 <= KB) split *= 2;
-    const double kb = per_sm * std::max(2.0 * bt, (16384 + bt * 128) / 56.0);
-    const double t = ceil_div(tiles * split, per_sm * sms) * (ceil_div(KB, split) * kb + 2000 + 10.0 * bt) +
-                     3000 + (split > 1 ? 1500 : 0);
-    if (t < best_t) {
-        int cols = 32;
-        while (cols < bt) cols *= 2;
-        const int data = std::max(stages * stage, bt * 512);
-        best = Plan{false, 0, bt, split, stages, cols, kSplitFixed + data};
+    const long tiles = (long)ceil_div(C, 128) * ceil_div(R, bt);
+    for (int split = 1; split <= 8 && split <= KB; split *= 2) {
+        const int gather = split > 1 ? split * ceil_div(bt, split) * 512 : 0;
+        for (int per_sm = 1; per_sm <= 2; ++per_sm) {
+            const int fit = ((per_sm == 2 ? kSplitHalf : kSmemMax) - kSplitFixed - gather) / stage;
+            const int stages = std::min(fit, kSplitMaxStages);
+            // the partial tile lies in the stages
+            if (stages < 3 || stages * stage < bt * 512) continue;
+            const long ctas = tiles * split;
+            const int waves = ceil_div(ctas, cluster_capacity(split, per_sm));
+            const int share = waves == 1 ? std::max(1, ceil_div(ctas, sms)) : per_sm;  // CTAs an SM runs at once
+            // the weights come from HBM once, about 25 bytes a cycle into one SM
+            const double kb = share * std::max({2.0 * bt, (16384 + bt * 128) / 64.0, 16384 / (25.0 * passes)});
+            double t = waves * (std::max(ceil_div(KB, split) * kb, 1500.0) + 3000 + 8.0 * bt +
+                                (split > 1 ? 1500 + 4.0 * bt : 0.0));
+            t = std::max(t, 2.0 * C * K / 3400) + 3000;  // HBM: about 3400 bytes a cycle
+            if (t < best_t) {
+                best_t = t;
+                int cols = 32;
+                while (cols < bt) cols *= 2;
+                best = Plan{false, 0, bt, split, stages, cols, kSplitFixed + gather + stages * stage};
+            }
+        }
     }
     return best;
 }
@@ -715,7 +1055,15 @@ cudaError_t product(const void* rp, long ldr, const void* cp, long ldc, const Ge
     const Plan p = plan_gemm<R_MN>(d.R, d.C, d.K);
     CUtensorMap tr, tc;
     if (p.pair) {
-        auto kernel = linear_pair_kernel<T, R_MN, C_MN>;
+        const bool tma_out = on_grid(e.out, e.ld_out) && on_grid(e.pre, e.ld_pre) && on_grid(e.res, e.ld_res);
+        OutMaps to;
+        if (tma_out) {
+            if (!out_map<T>(&to.out, e.out, e.ld_out, d) ||
+                !out_map<T>(&to.pre, e.pre ? e.pre : e.out, e.pre ? e.ld_pre : e.ld_out, d) ||
+                !out_map<T>(&to.res, e.res ? e.res : e.out, e.res ? e.ld_res : e.ld_out, d))
+                return cudaErrorInvalidValue;
+        }
+        auto kernel = tma_out ? linear_pair_kernel<T, R_MN, C_MN, true> : linear_pair_kernel<T, R_MN, C_MN, false>;
         if (cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), PairCfg::SMEM_BYTES))
             return err;
         if (!operand_map<T, R_MN>(&tr, rp, ldr, d.R, d.K, 128) ||
@@ -723,8 +1071,8 @@ cudaError_t product(const void* rp, long ldr, const void* cp, long ldc, const Ge
             return cudaErrorInvalidValue;
         const long tiles = (long)ceil_div(d.R, 256) * ceil_div(d.C, p.bn);
         const int pairs = (int)std::min<long>(num_sms() / 2, tiles);
-        return launch_cluster(kernel, dim3(2 * pairs), 2, PairCfg::THREADS, PairCfg::SMEM_BYTES, st, tr, tc, d,
-                              e, p.bn);
+        return launch_cluster(kernel, dim3(2 * pairs), 2, PairCfg::THREADS, PairCfg::SMEM_BYTES, st, tr, tc,
+                              to, d, e, p.bn);
     }
     auto kernel = linear_split_kernel<T, C_MN, R_MN>;
     if (cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), p.smem)) return err;
@@ -744,7 +1092,8 @@ template <typename T>
 cudaError_t forward(const LinearArgs& a, cudaStream_t st) {
     const GemmDims d{a.M, a.N, a.K, a.status};
     Epilogue e{a.bias, a.res, a.y, a.pre, a.ldr, a.ldy, a.ldp, a.M, a.N, a.act, 0};
-    e.vec = quad(a.res, a.ldr) && quad(a.y, a.ldy) && quad(a.pre, a.ldp);
+    e.vec = quad(a.res, a.ldr) && quad(a.y, a.ldy) && quad(a.pre, a.ldp) &&
+            (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0;
     return product<T, false, false>(a.x, a.ldx, a.w, a.ldw, d, e, st);
 }
 

@@ -121,6 +121,29 @@ __device__ __forceinline__ uint4 narrow(const f32x2 (&v)[kPairs<T>]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Four fp32 values rounded to a 16-bit type, packed.
+template <typename T>
+__device__ __forceinline__ uint2 narrow4(const float (&v)[4]) {
+    uint2 r;
+    if constexpr (is_half<T>()) {
+        const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+        r.x = *reinterpret_cast<const uint32_t*>(&a);
+        r.y = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        r.x = *reinterpret_cast<const uint32_t*>(&a);
+        r.y = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 narrow8(const float* v) {
+    const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
+    const uint2 x = narrow4<T>(a), y = narrow4<T>(b);
+    return make_uint4(x.x, x.y, y.x, y.y);
+}
+
 inline int esize(int dtype) { return dtype == MOE_T_F32 ? 4 : 2; }
 
 }  // namespace moe
