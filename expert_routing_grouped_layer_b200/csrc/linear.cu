@@ -145,8 +145,9 @@ __device__ __forceinline__ float act_f(float z) {
     return z;
 }
 
-__device__ __forceinline__ float act_slope(float z, int act) {
-    switch (act) {
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+    switch (ACT) {
     case MOE_ACT_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     case MOE_ACT_SILU: {
         const float s = sigmoid_f(z);
@@ -167,7 +168,7 @@ __device__ __forceinline__ float act_slope(float z, int act) {
 
 // Calls f with the activation as a compile-time constant: one branch for a group of values.
 template <typename F>
-__device__ __forceinline__ void with_act(int act, F&& f) {
+__host__ __device__ __forceinline__ void with_act(int act, F&& f) {
     switch (act) {
     case MOE_ACT_RELU: f(std::integral_constant<int, MOE_ACT_RELU>()); break;
     case MOE_ACT_SILU: f(std::integral_constant<int, MOE_ACT_SILU>()); break;
@@ -885,44 +886,75 @@ struct ActBwd {
     int M, N, act, rows;  // rows per CTA
 };
 
-// CTA (x, y): 32 VEC columns x `rows` rows; warp w takes rows w, w + 8, ... The column
-// sums of the unrounded products stay in registers, then cross the warps once.
-template <typename T, int VEC>
+// VEC elements of dy and pre into g; their fp32 products are added to sum.
+template <typename T, int VEC, int ACT>
+__device__ __forceinline__ Pack<T, VEC> act_grad(const Pack<T, VEC>& a, const Pack<T, VEC>& z, float (&sum)[VEC]) {
+    Pack<T, VEC> o;
+    float v[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        v[j] = to_f32<T>(a.v[j]);
+        if (ACT != MOE_ACT_NONE) v[j] *= act_slope<ACT>(to_f32<T>(z.v[j]));
+        sum[j] += v[j];
+    }
+    if constexpr (VEC == 8) {
+        *reinterpret_cast<uint4*>(&o) = narrow8<T>(v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) o.v[j] = from_f32<T>(v[j]);
+    }
+    return o;
+}
+
+// CTA (x, y): 32 VEC columns x `rows` rows; warp w takes rows w, w + 8, ..., four at a time
+// so that eight loads are in flight (one row at a time: 91 us instead of 70 for 8192 x 7168 SiLU).
+// The column sums of the unrounded products stay in registers, then cross the warps once.
+template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(256) linear_act_bwd_kernel(ActBwd p) {
     pdl_wait();
     pdl_trigger();
     __shared__ float red[8][32 * VEC];
+    using V = Pack<T, VEC>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = (blockIdx.x * 32 + lane) * VEC;
     const long m0 = (long)blockIdx.y * p.rows, m1 = min((long)p.M, m0 + p.rows);
     float sum[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) sum[j] = 0.f;
-    const bool whole = col + VEC <= p.N;
-    if (col < p.N) {
-        for (long m = m0 + warp; m < m1; m += 8) {
-            const T* dy = static_cast<const T*>(p.dy) + m * p.lddy + col;
-            const T* pre = static_cast<const T*>(p.pre) + m * p.ldp + col;
-            Pack<T, VEC> a, z, o;
-            if (VEC == 1 || whole) {
-                a = *reinterpret_cast<const Pack<T, VEC>*>(dy);
-                if (p.act != MOE_ACT_NONE) z = *reinterpret_cast<const Pack<T, VEC>*>(pre);
-            } else {
+    const T* dy = static_cast<const T*>(p.dy) + col;
+    const T* pre = static_cast<const T*>(p.pre) + col;
+    T* g = static_cast<T*>(p.g) + col;
+    constexpr int U = 4;
+    if (col + VEC <= p.N) {
+        for (long m = m0 + warp; m < m1; m += 8 * U) {
+            V a[U], z[U];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    a.v[j] = col + j < p.N ? dy[j] : from_f32<T>(0.f);
-                    z.v[j] = p.act != MOE_ACT_NONE && col + j < p.N ? pre[j] : from_f32<T>(0.f);
+            for (int i = 0; i < U; ++i) {
+                const long r = m + 8 * i;
+                if (r < m1) {
+                    a[i] = *reinterpret_cast<const V*>(dy + r * p.lddy);
+                    if (ACT != MOE_ACT_NONE) z[i] = *reinterpret_cast<const V*>(pre + r * p.ldp);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                float v = to_f32<T>(a.v[j]);
-                if (p.act != MOE_ACT_NONE) v *= act_slope(to_f32<T>(z.v[j]), p.act);
-                sum[j] += v;
-                o.v[j] = from_f32<T>(v);
+            for (int i = 0; i < U; ++i) {
+                const long r = m + 8 * i;
+                if (r >= m1) continue;
+                const V o = act_grad<T, VEC, ACT>(a[i], z[i], sum);
+                if (p.g) *reinterpret_cast<V*>(g + r * p.ldg) = o;
             }
-            // the workspace's rows are padded to whole vectors
-            if (p.g) *reinterpret_cast<Pack<T, VEC>*>(static_cast<T*>(p.g) + m * p.ldg + col) = o;
+        }
+    } else if (col < p.N) {  // the last, partial vector of a row; the workspace's rows are whole vectors
+        for (long m = m0 + warp; m < m1; m += 8) {
+            V a, z;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const bool in = col + j < p.N;
+                a.v[j] = in ? dy[m * p.lddy + j] : from_f32<T>(0.f);
+                z.v[j] = ACT != MOE_ACT_NONE && in ? pre[m * p.ldp + j] : from_f32<T>(0.f);
+            }
+            const V o = act_grad<T, VEC, ACT>(a, z, sum);
+            if (p.g) *reinterpret_cast<V*>(g + m * p.ldg) = o;
         }
     }
     if (!p.part) return;
@@ -1012,7 +1044,7 @@ Plan plan_gemm(int R, int C, int K) {
     for (int bn = 256; bn >= 64; bn -= 32) {
         const long tiles = (long)ceil_div(R, 256) * ceil_div(C, bn);
         const double kb = std::max(2.0 * bn, (16384 + bn * 64) / 64.0);
-        const double t = ceil_div(tiles, sms / 2) * (KB * kb + 400) + 12.0 * bn + 4000;
+        const double t = ceil_div(tiles, sms / 2) * (KB * kb + 400) + 45.0 * bn + 8000;
         if (t < best_t) {
             best_t = t;
             best = Plan{true, bn};
@@ -1034,9 +1066,8 @@ Plan plan_gemm(int R, int C, int K) {
             const int share = waves == 1 ? std::max(1, ceil_div(ctas, sms)) : per_sm;  // CTAs an SM runs at once
             // the weights come from HBM once, about 25 bytes a cycle into one SM
             const double kb = share * std::max({2.0 * bt, (16384 + bt * 128) / 64.0, 16384 / (25.0 * passes)});
-            double t = waves * (std::max(ceil_div(KB, split) * kb, 1500.0) + 3000 + 8.0 * bt +
-                                (split > 1 ? 1500 + 4.0 * bt : 0.0));
-            t = std::max(t, 2.0 * C * K / 3400) + 3000;  // HBM: about 3400 bytes a cycle
+            const double t = waves * (std::max(ceil_div(KB, split) * kb, 1500.0) + 4000 + 8.0 * bt +
+                                      30.0 * bt / split + (split > 1 ? 1500 + 4.0 * bt : 0.0)) + 6000;
             if (t < best_t) {
                 best_t = t;
                 int cols = 32;
@@ -1127,8 +1158,10 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t st) {
         p.rows = act_rows(a.M, a.N, vec ? 8 : 1);
         const int chunks = ceil_div(a.M, p.rows);
         const dim3 grid(ceil_div(a.N, vec ? 256 : 32), chunks);
-        if (vec) launch_pdl(linear_act_bwd_kernel<T, 8>, grid, 256, 0, st, p);
-        else launch_pdl(linear_act_bwd_kernel<T, 1>, grid, 256, 0, st, p);
+        with_act(a.act, [&](auto act) {
+            if (vec) launch_pdl(linear_act_bwd_kernel<T, 8, act.value>, grid, 256, 0, st, p);
+            else launch_pdl(linear_act_bwd_kernel<T, 1, act.value>, grid, 256, 0, st, p);
+        });
         if (a.db)
             launch_pdl(linear_bias_kernel, ceil_div(a.N, 32), 256, 0, st, (const float*)p.part, chunks, a.N, a.db);
         if (cudaError_t err = cudaGetLastError()) return err;
