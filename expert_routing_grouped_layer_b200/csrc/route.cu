@@ -18,6 +18,7 @@
 // the bytes.
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "sm100.cuh"
@@ -62,8 +63,23 @@ __device__ __forceinline__ double warp_sum(double v) {
 }
 
 // Scores. m and z: the row's largest logit and sum of exponentials (softmax).
+// For the order alone: exponentials and reciprocals of a few units of 2^-24, scaled by the
+// argument (|l| s (1 - s) and |l - m| s stay below 0.4), see the bound in the kernel.
+template <int FN>
+__device__ __forceinline__ float score_fast(float l, float m, float inv_z) {
+    if (FN == MOE_SCORE_SIGMOID) return __fdividef(1.0f, 1.0f + __expf(-l));
+    if (FN == MOE_SCORE_SQRTSOFTPLUS) return sqrtf(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
+    return __expf(l - m) * inv_z;
+}
+template <typename F>
+__device__ __forceinline__ void with_score(int fn, F&& f) {
+    if (fn == MOE_SCORE_SIGMOID) f(std::integral_constant<int, MOE_SCORE_SIGMOID>());
+    else if (fn == MOE_SCORE_SQRTSOFTPLUS) f(std::integral_constant<int, MOE_SCORE_SQRTSOFTPLUS>());
+    else f(std::integral_constant<int, MOE_SCORE_SOFTMAX>());
+}
+
 __device__ __forceinline__ float score_f(float l, int fn, float m, float inv_z) {
-    if (fn == MOE_SCORE_SIGMOID) return __fdividef(1.0f, 1.0f + expf(-l));
+    if (fn == MOE_SCORE_SIGMOID) return 1.0f / (1.0f + expf(-l));
     if (fn == MOE_SCORE_SQRTSOFTPLUS) return sqrtf(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
     return expf(l - m) * inv_z;
 }
@@ -201,6 +217,20 @@ __device__ __forceinline__ float chosen_weight(float l, bool valid, int fn, int 
     return sum > 0.f ? s / sum : 0.f;
 }
 
+template <int VEC>
+__device__ __forceinline__ void load_bias(float* b, const float* p) {
+    if constexpr (VEC % 4 == 0) {  // 16-byte aligned where the logits' vectors are used
+#pragma unroll
+        for (int v = 0; v < VEC; v += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(p + v);
+            b[v] = f.x; b[v + 1] = f.y; b[v + 2] = f.z; b[v + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) b[v] = p[v];
+    }
+}
+
 // Lane (g, sub) of L lanes per group holds the group's elements (sub + L i) VEC + v:
 // a group's two largest come from the lanes of that group alone, and without groups
 // (L = 32) a load instruction covers consecutive elements.
@@ -225,45 +255,52 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
     for (int i = 0; i < NI; ++i)
         if (sub + i * L < nvec) raw[i] = reinterpret_cast<const Pack<T, VEC>*>(row + e0)[i * L];
     const bool by_logit = !p.bias && p.n_group == 1;
-    float sel[J];
+    float sel[J];  // logits, then s' (or the logits, by_logit); -inf: masked or no element
     bool bad = false;
-    float lm = -kInf;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            float l = sub + i * L < nvec ? to_f32<T>(raw[i].v[v]) + 0.0f : -kInf;
+            const float l = sub + i * L < nvec ? to_f32<T>(raw[i].v[v]) + 0.0f : -kInf;
             bad |= !(l < kInf);
-            lm = fmaxf(lm, l);
             sel[i * VEC + v] = l;
         }
     }
     // the row's maximum and sum of exponentials (softmax), or the largest score's bound
     float m = 0.f, z = 1.f, scale = 1.f;
     if (p.score_fn != MOE_SCORE_SIGMOID) {
+        float lm = sel[0];
+#pragma unroll
+        for (int j = 1; j < J; ++j) lm = fmaxf(lm, sel[j]);
         const float top = warp_max(bad ? -kInf : lm);
         if (p.score_fn == MOE_SCORE_SOFTMAX) {
             m = top == -kInf ? 0.f : top;
             float zs = 0.f;
 #pragma unroll
-            for (int j = 0; j < J; ++j) zs += expf(sel[j] - m);
+            for (int j = 0; j < J; ++j) zs += __expf(sel[j] - m);
             z = warp_sum(zs);
         } else {
             scale = fmaxf(1.f, sqrtf(fmaxf(top, 0.f) + 1.f));
         }
     }
     if (!by_logit) {
-        const float inv_z = 1.0f / z;
+        const float inv_z = z > 0.f ? 1.0f / z : 0.f;  // 0: every expert is masked
+        float bias[J];
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
+        for (int j = 0; j < J; ++j) bias[j] = 0.f;
+        if (p.bias) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const int j = i * VEC + v;
-                const float b = p.bias && sub + i * L < nvec ? p.bias[e0 + i * L * VEC + v] : 0.f;
-                bad |= !(b < kInf);
-                sel[j] = sel[j] == -kInf || b == -kInf ? -kInf : score_f(sel[j], p.score_fn, m, inv_z) + b;
-            }
+            for (int i = 0; i < NI; ++i)
+                if (sub + i * L < nvec) load_bias<VEC>(bias + i * VEC, p.bias + e0 + i * L * VEC);
         }
+        with_score(p.score_fn, [&](auto fn) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float s = score_fast<fn.value>(sel[j], m, inv_z) + bias[j];  // -inf with the bias
+                bad |= !(s < kInf);
+                sel[j] = sel[j] == -kInf ? -kInf : s;
+            }
+        });
     }
     if (__any_sync(kFull, bad)) {  // a NaN or +inf among the row's logits or the biases
         if (lane < p.k) {
@@ -274,7 +311,7 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
     }
     // |computed s' - s'| <= eps * max(scale, |s'|): a few units of 2^-24 for the sigmoid and
     // sqrt-softplus, up to J + 5 more for the softmax's sum
-    const float eps = p.score_fn == MOE_SCORE_SOFTMAX ? 7.7e-6f : 4.8e-7f;
+    const float eps = p.score_fn == MOE_SCORE_SOFTMAX ? 9.6e-6f : 6.0e-7f;
 
     uint32_t kept = kFull;
     if (p.n_group > 1) {
@@ -295,7 +332,8 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
             const float o = __shfl_sync(kFull, gs, h * L);
             rank += (o > gs || (o == gs && h < g)) ? 1 : 0;
         }
-        const bool real = g < p.n_group, keep = real && rank < p.topk_group;
+        const bool real = g < p.n_group;
+        bool keep = real && rank < p.topk_group;
         const float lo = -warp_max(keep ? -gs : -kInf);          // smallest kept
         const float hi = warp_max(real && !keep ? gs : -kInf);   // largest left out
         const float mag = warp_max(real && b1 != -kInf ? fmaxf(fabsf(b1), b2 == -kInf ? 0.f : fabsf(b2)) : 0.f);
@@ -304,12 +342,9 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
             const double zd = p.score_fn == MOE_SCORE_SOFTMAX ? row_z<T>(row, p.E, m) : 1.0;
             kept = groups_exact<T>(Row<T>{row, p.bias, p.E, gsz, p.score_fn, m, zd, kFull}, p.n_group,
                                    p.topk_group);
-        } else {
-            kept = 0;
-            for (int h = 0; h < p.n_group; ++h)
-                kept |= (__shfl_sync(kFull, (int)keep, h * L) & 1) << h;
+            keep = real && ((kept >> g) & 1u);
         }
-        if (!((kept >> (g < p.n_group ? g : 0)) & 1u)) {
+        if (!keep) {
 #pragma unroll
             for (int j = 0; j < J; ++j) sel[j] = -kInf;
         }
@@ -317,28 +352,34 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
 
     // Each lane caches its two best elements; a round is one warp maximum over the
     // lanes' heads. The winner pops its head and rescans when its cache is empty.
-    u64 avail = 0;
+    // Within a lane the expert grows with j, so the first of equal keys is the lower.
+    typedef typename std::conditional<(J > 32), u64, uint32_t>::type Bits;
+    Bits avail = 0;
 #pragma unroll
     for (int j = 0; j < J; ++j)
-        if (sel[j] != -kInf) avail |= 1ull << j;
+        if (sel[j] != -kInf) avail |= Bits(1) << j;
+    auto expert = [&](int j) { return e0 + (j / VEC) * L * VEC + j % VEC; };
     uint32_t k1, k2;
-    int j1, j2;
+    int e1, e2;
+    Bits bit1, bit2;
     auto refill = [&]() {
-        k1 = k2 = 0u;
-        j1 = j2 = -1;
+        float v1 = -kInf, v2 = -kInf;
+        e1 = e2 = INT_MAX;
+        bit1 = bit2 = 0;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const uint32_t kk = (avail >> j) & 1ull ? key_of(sel[j]) : 0u;
-            if (kk > k1) {
-                k2 = k1; j2 = j1;
-                k1 = kk; j1 = j;
-            } else if (kk > k2) {
-                k2 = kk; j2 = j;
-            }
+            const float v = avail & (Bits(1) << j) ? sel[j] : -kInf;
+            const bool first = v > v1, second = v > v2;
+            v2 = first ? v1 : (second ? v : v2);
+            e2 = first ? e1 : (second ? expert(j) : e2);
+            bit2 = first ? bit1 : (second ? Bits(1) << j : bit2);
+            v1 = first ? v : v1;
+            e1 = first ? expert(j) : e1;
+            bit1 = first ? Bits(1) << j : bit1;
         }
+        k1 = bit1 ? key_of(v1) : 0u;
+        k2 = bit2 ? key_of(v2) : 0u;
     };
-    // within a lane the element index grows with j, so the first of equal keys is the lower
-    auto expert = [&](int j) { return e0 + (j / VEC) * L * VEC + j % VEC; };
     refill();
     int my_e = -1;
     uint32_t my_key = 0u, last = 0u;
@@ -346,21 +387,17 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
         const uint32_t top = __reduce_max_sync(kFull, k1);
         if (top == 0u) break;  // fewer than k experts are left
         const uint32_t who = __ballot_sync(kFull, k1 == top);
-        int win = __ffs(who) - 1;
-        if (who & (who - 1)) {  // equal keys in several lanes: the lowest index
-            const int low = __reduce_min_sync(kFull, k1 == top ? expert(j1) : INT_MAX);
-            win = __ffs(__ballot_sync(kFull, k1 == top && expert(j1) == low)) - 1;
-        }
-        const int e = __shfl_sync(kFull, j1 >= 0 ? expert(j1) : -1, win);
+        int e = __shfl_sync(kFull, e1, __ffs(who) - 1);
+        if (who & (who - 1)) e = __reduce_min_sync(kFull, k1 == top ? e1 : INT_MAX);  // the lowest index
         if (lane == r) {
             my_e = e;
             my_key = top;
         }
         last = top;
-        if (lane == win) {
-            avail &= ~(1ull << j1);
-            k1 = k2; j1 = j2;
-            k2 = 0u; j2 = -1;
+        if (e1 == e) {
+            avail &= ~bit1;
+            k1 = k2; e1 = e2; bit1 = bit2;
+            k2 = 0u; e2 = INT_MAX; bit2 = 0;
             if (k1 == 0u && avail) refill();
         }
     }
@@ -383,7 +420,7 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
         if (k1 != 0u && value_of(k1) >= cut) {
 #pragma unroll
             for (int j = 0; j < J; ++j)
-                if (((avail >> j) & 1ull) && sel[j] >= cut) {
+                if ((avail & (Bits(1) << j)) && sel[j] >= cut) {
                     const int e = expert(j);
                     near |= !(to_f32<T>(row[e]) + 0.0f == ll && (p.bias ? p.bias[e] : 0.f) == lb);
                 }
@@ -480,7 +517,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwd p) {
             float zs = 0.f;
 #pragma unroll
             for (int j = 0; j < NI * VEC; ++j) {
-                s[j] = expf(s[j] - m);
+                s[j] = __expf(s[j] - m);
                 zs += s[j];
             }
             z = warp_sum(zs);
@@ -558,7 +595,7 @@ cudaError_t launch_route(const moe_config* c, int dtype, const void* logits, lon
                         c->n_group, c->topk_group, c->norm_topk_prob, c->score_fn,
                         c->routed_scaling_factor};
     const int es = esize(dtype);
-    const bool vec = (p.E / p.n_group) % (16 / es) == 0 && rows16(logits, ld, es);
+    const bool vec = (p.E / p.n_group) % (16 / es) == 0 && rows16(logits, ld, es) && rows16(bias, 4, 4);
     if (dtype == MOE_T_BF16) fwd_type<__nv_bfloat16>(p, vec, st);
     else if (dtype == MOE_T_F16) fwd_type<__half>(p, vec, st);
     else fwd_type<float>(p, vec, st);
