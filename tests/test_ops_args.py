@@ -178,3 +178,6 @@ def test_binding_checks_layout():
         moe._matrix("x", _Fake((4, 64), (64, 1), torch.float64))
     with pytest.raises(ValueError, match="a matrix"):
         moe._matrix("x", _Fake((64,), (1,)))
+    with pytest.raises(ValueError, match="adjacent"):
+        moe._matrix("x", _Fake((4, 64), (64, 2)))
+    assert moe._matrix("x", _Fake((4, 64), (72, 1))) == (0, 0, bf, 4, 64, 4096, 72)
