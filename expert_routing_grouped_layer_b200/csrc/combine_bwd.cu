@@ -86,19 +86,20 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const uint4* __restric
             }
         }
     }
-    if (!DOT) return;
+    if constexpr (DOT) {
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-    if constexpr (WPP == 1) {
-        if (in && lane == 0) dw[pair] = dot;
-    } else {
-        if (lane == 0) part[warp] = dot;
-        __syncthreads();
-        if (in && lane == 0 && warp % WPP == 0) {
-            float s = 0.f;
+        for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
+        if constexpr (WPP == 1) {
+            if (in && lane == 0) dw[pair] = dot;
+        } else {
+            if (lane == 0) part[warp] = dot;
+            __syncthreads();
+            if (in && lane == 0 && warp % WPP == 0) {
+                float s = 0.f;
 #pragma unroll
-            for (int i = 0; i < WPP; ++i) s += part[warp + i];
-            dw[pair] = s;
+                for (int i = 0; i < WPP; ++i) s += part[warp + i];
+                dw[pair] = s;
+            }
         }
     }
 }

@@ -109,10 +109,10 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kSqrt2OverPi = 0.79788456080286536f;
 constexpr float kGeluCubic = 0.044715f;
 
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+__device__ __forceinline__ float sigmoid_f(float z) { return rcp_approx(1.0f + exp_approx(-z)); }
 
 // tanh through one exponential: accurate to a few units of 2^-24 of 1, saturating cleanly
-__device__ __forceinline__ float tanh_f(float u) { return 1.0f - __fdividef(2.0f, 1.0f + __expf(2.0f * u)); }
+__device__ __forceinline__ float tanh_f(float u) { return 1.0f - 2.0f * rcp_approx(1.0f + exp_approx(2.0f * u)); }
 
 // The normal distribution's Phi(z) and exp(-z^2 / 2) by Abramowitz and Stegun's 7.1.26 (erfc
 // as a polynomial in 1 / (1 + 0.3275911 x) times exp(-x^2), |error| <= 1.5e-7): no
@@ -120,8 +120,8 @@ __device__ __forceinline__ float tanh_f(float u) { return 1.0f - __fdividef(2.0f
 // it the GELU epilogue took 11.6 us a tile.
 __device__ __forceinline__ float normal_cdf(float z, float& gauss) {
     const float x = fabsf(z) * kSqrtHalf;
-    gauss = __expf(-x * x);
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    gauss = exp_approx(-x * x);
+    const float t = rcp_approx(fmaf(0.3275911f, x, 1.0f));
     float p = fmaf(t, 1.061405429f, -1.453152027f);
     p = fmaf(t, p, 1.421413741f);
     p = fmaf(t, p, -0.284496736f);

@@ -67,9 +67,9 @@ __device__ __forceinline__ double warp_sum(double v) {
 // argument (|l| s (1 - s) and |l - m| s stay below 0.4), see the bound in the kernel.
 template <int FN>
 __device__ __forceinline__ float score_fast(float l, float m, float inv_z) {
-    if (FN == MOE_SCORE_SIGMOID) return __fdividef(1.0f, 1.0f + __expf(-l));
+    if (FN == MOE_SCORE_SIGMOID) return rcp_approx(1.0f + exp_approx(-l));
     if (FN == MOE_SCORE_SQRTSOFTPLUS) return sqrtf(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
-    return __expf(l - m) * inv_z;
+    return exp_approx(l - m) * inv_z;
 }
 template <typename F>
 __device__ __forceinline__ void with_score(int fn, F&& f) {
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
             m = top == -kInf ? 0.f : top;
             float zs = 0.f;
 #pragma unroll
-            for (int j = 0; j < J; ++j) zs += __expf(sel[j] - m);
+            for (int j = 0; j < J; ++j) zs += exp_approx(sel[j] - m);
             z = warp_sum(zs);
         } else {
             scale = fmaxf(1.f, sqrtf(fmaxf(top, 0.f) + 1.f));
@@ -491,6 +491,13 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwd p) {
     const int nvec = p.E / VEC;
     const bool dense = p.score_fn == MOE_SCORE_SOFTMAX && !p.norm;
 
+    // the row's loads go out before the slots', whose logits hang on the indices
+    Pack<T, VEC> raw[NI];
+    if (dense) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (lane + 32 * i < nvec) raw[i] = reinterpret_cast<const Pack<T, VEC>*>(row)[lane + 32 * i];
+    }
     int e = lane < p.k ? p.idx[t * p.k + lane] : -1;
     if (e < 0 || e >= p.E) e = -1;
     const bool valid = e >= 0;
@@ -505,11 +512,9 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwd p) {
             float top = -kInf;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                Pack<T, VEC> raw;
-                if (lane + 32 * i < nvec) raw = reinterpret_cast<const Pack<T, VEC>*>(row)[lane + 32 * i];
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
-                    s[i * VEC + v] = lane + 32 * i < nvec ? to_f32<T>(raw.v[v]) : -kInf;
+                    s[i * VEC + v] = lane + 32 * i < nvec ? to_f32<T>(raw[i].v[v]) : -kInf;
                     top = fmaxf(top, s[i * VEC + v]);
                 }
             }
@@ -517,7 +522,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwd p) {
             float zs = 0.f;
 #pragma unroll
             for (int j = 0; j < NI * VEC; ++j) {
-                s[j] = __expf(s[j] - m);
+                s[j] = exp_approx(s[j] - m);
                 zs += s[j];
             }
             z = warp_sum(zs);
@@ -530,7 +535,8 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwd p) {
     float d = p.norm ? w * (g - dot) : w * g;
     if (p.score_fn != MOE_SCORE_SOFTMAX) d *= log_slope(l, p.score_fn);
     // an expert in several slots gets the slots' sum, added in slot order
-    const uint32_t same = __match_any_sync(kFull, valid ? e : -1 - lane);
+    uint32_t same = 0;
+    for (int c = 0; c < p.k; ++c) same |= (__shfl_sync(kFull, e, c) == e ? 1u : 0u) << c;
     if (__any_sync(kFull, valid && (same & (same - 1)))) {
         float sum = 0.f;
         for (int c = 0; c < p.k; ++c) {
@@ -546,8 +552,15 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwd p) {
     for (int i = 0; i < NI; ++i) {
         if (lane + 32 * i >= nvec) continue;
         Pack<T, VEC> o;
+        float v[VEC];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) o.v[v] = from_f32<T>(dense && any ? s[i * VEC + v] * back : 0.f);
+        for (int j = 0; j < VEC; ++j) v[j] = dense && any ? s[i * VEC + j] * back : 0.f;
+        if constexpr (VEC == 8) {
+            *reinterpret_cast<uint4*>(&o) = narrow8<T>(v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) o.v[j] = from_f32<T>(v[j]);
+        }
         reinterpret_cast<Pack<T, VEC>*>(out)[lane + 32 * i] = o;
     }
     __syncwarp();
