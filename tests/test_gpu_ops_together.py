@@ -1,0 +1,154 @@
+"""The operators around the experts in one training step of a block, as a program uses them:
+norm -> router product -> routing -> permutation -> experts -> combine, then back through
+the combine, the routing, the router product and the norm (the experts frozen), and a
+dense layer with its residual beside them. Checked against 64-bit autograd over the same
+inputs, with the experts' output rows and the chosen experts taken from the run.
+
+Tolerance: relative L2. The run rounds to bf16 the normalised rows, the logits, the combined
+output's gradient into rows, dlogits, and each matrix product's output: at most 7 roundings
+on the way to any gradient, each at most 2^-8 of its value, and a logit's rounding error
+(2^-8 of about 2) reaches a weight undiminished: 9 * 2^-8 = 3.5e-2 in all."""
+import pytest
+import torch
+
+import expert_routing_grouped_layer_b200 as moe
+import ops_reference as ref
+from expert_routing_grouped_layer_b200 import workloads as W
+
+pytestmark = pytest.mark.gpu
+TOL = 9 * 2.0 ** -8
+BF = torch.bfloat16
+
+
+class Block:
+    """A block's parameters, workspaces and gradients, allocated once."""
+
+    def __init__(self, T, seed):
+        self.cfg = W.CONFIGS["tiny_bf16"].replace(T=T, n_group=4, topk_group=2)
+        c = self.cfg
+        H, E, k, I, S = (c.hidden, c.n_routed_experts, c.num_experts_per_tok, c.moe_intermediate_size,
+                         c.n_shared_experts)
+        N = T * k
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rand = lambda *s: torch.randn(*s, generator=g, device="cuda")
+        e = lambda *s, t=BF: torch.empty(*s, dtype=t, device="cuda")
+        self.x, self.dout, self.ddense = rand(T, H).to(BF), rand(T, H).to(BF), rand(T, H).to(BF)
+        self.nw, self.nb = 1 + 0.2 * rand(H), 0.1 * rand(H)
+        self.wr = (1.7 * rand(E, H) * H ** -0.5).to(BF)
+        self.bias = 0.1 * rand(E)
+        self.wd, self.bd = (rand(H, H) * H ** -0.5).to(BF), 0.1 * rand(H)
+        self.experts = W.make_weights(c, "cuda")
+        f, i = torch.float32, torch.int32
+        self.ws = e(moe.moe_workspace_bytes(c, T), t=torch.uint8)
+        self.status = torch.zeros(1, dtype=i, device="cuda")
+        self.h, self.mean, self.rstd = e(T, H), e(T, t=f), e(T, t=f)
+        self.logits, self.idx, self.w = e(T, E), e(T, k, t=i), e(T, k, t=f)
+        self.off, self.pairs, self.row_of = e(E + 1, t=i), e(N, t=i), e(N, t=i)
+        self.y, self.sy, self.out = e(N, H), e(S, T, H), e(T, H)
+        self.dense, self.pre = e(T, H), e(T, H)
+        self.dy, self.dw, self.dlogits = torch.zeros(N, H, dtype=BF, device="cuda"), e(T, k, t=f), e(T, E)
+        self.dh, self.dwr = e(T, H), e(E, H)
+        self.dx, self.dnw, self.dnb = e(T, H), e(H, t=f), e(H, t=f)
+        self.dhd, self.dwd, self.dbd = e(T, H), e(H, H), e(H, t=f)
+        need = max(moe.moe_norm_backward_workspace_bytes(T, H),
+                   moe.moe_linear_backward_workspace_bytes(T, H, H, "gelu"))
+        self.ops_ws = e(need, t=torch.uint8)
+
+    def step(self):
+        c, T = self.cfg, self.cfg.T
+        moe.moe_norm(self.x, self.nw, self.nb, 1e-6, self.h, self.mean, self.rstd)
+        moe.moe_linear(self.h, self.wr, None, None, self.logits, dev_status=self.status)
+        moe.moe_route(c, self.logits, self.bias, self.idx, self.w)
+        moe.moe_permute(c, self.idx, T, self.off, self.pairs, self.row_of, self.status, self.ws)
+        moe.moe_grouped_swiglu(c, self.h, T, self.pairs, self.off, self.experts, self.y, self.sy, self.ws,
+                               self.status)
+        moe.moe_combine(c, self.y, self.sy, self.row_of, self.w, T, self.out)
+        moe.moe_linear(self.h, self.wd, self.bd, self.x, self.dense, self.pre, act="gelu",
+                       dev_status=self.status)
+        # and back
+        moe.moe_combine_backward(c, self.dout, self.y, self.row_of, self.w, self.dy, self.dw)
+        moe.moe_route_backward(c, self.logits, self.idx, self.dw, self.dlogits)
+        moe.moe_linear_backward(self.dlogits, self.h, self.wr, None, self.dh, self.dwr, None, self.ops_ws,
+                                dev_status=self.status)
+        moe.moe_norm_backward(self.dh, self.x, self.nw, self.mean, self.rstd, self.dx, self.dnw, self.dnb,
+                              self.ops_ws)
+        moe.moe_linear_backward(self.ddense, self.h, self.wd, self.pre, self.dhd, self.dwd, self.dbd,
+                                self.ops_ws, act="gelu", dev_status=self.status)
+
+    def results(self):
+        return [self.out, self.dense, self.idx, self.w, self.dy, self.dw, self.dlogits, self.dwr, self.dx,
+                self.dnw, self.dnb, self.dhd, self.dwd, self.dbd]
+
+
+def _rel(a, b):
+    return ((a.double() - b).norm() / b.norm()).item()
+
+
+@pytest.mark.parametrize("T", [1, 50, 700])
+def test_block_step(T):
+    b = Block(T, T)
+    b.step()
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
+    x, nw, nb, wr, wd, bd = (t.double().requires_grad_(True) for t in (b.x, b.nw, b.nb, b.wr, b.wd, b.bd))
+    mean = x.mean(1, keepdim=True)
+    h = (x - mean) / torch.sqrt(((x - mean) ** 2).mean(1, keepdim=True) + 1e-6) * nw + nb
+    w = ref.route_weights(b.cfg, h @ wr.t(), b.idx)
+    k = b.cfg.num_experts_per_tok
+    rows = b.y.double()[b.row_of.long()].view(T, k, -1)
+    out = (w[:, :, None] * rows).sum(1)
+    assert _rel(b.out.float(), (out + b.sy.double().sum(0)).detach()) < TOL
+    assert _rel(b.w, w.detach()) < TOL
+    gx, gnw, gnb, gwr = torch.autograd.grad((out * b.dout.double()).sum(), (x, nw, nb, wr), retain_graph=True)
+    for got, want in ((b.dx, gx), (b.dnw, gnw), (b.dnb, gnb), (b.dwr, gwr)):
+        assert _rel(got, want) < TOL
+    dense = ref.act(h @ wd.t() + bd, "gelu") + x
+    assert _rel(b.dense, dense.detach()) < TOL
+    gh, gwd, gbd = torch.autograd.grad((dense * b.ddense.double()).sum(), (h, wd, bd))
+    for got, want in ((b.dhd, gh), (b.dwd, gwd), (b.dbd, gbd)):
+        assert _rel(got, want) < TOL
+
+
+def test_block_step_captured():
+    """The whole step in a graph, replayed on new inputs, gives the bits of direct calls."""
+    s = torch.cuda.Stream()
+    b = Block(130, 7)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        b.step()
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            b.step()
+        b.x.neg_()
+        b.dout.mul_(2)
+        g.replay()
+        s.synchronize()
+        got = [r.clone() for r in b.results()]
+        for r in b.results():
+            r.zero_()
+        b.step()
+        s.synchronize()
+    assert all(torch.equal(a, r) for a, r in zip(got, b.results()))
+    assert b.status.item() == 0
+
+
+def test_two_blocks_at_once():
+    """Two steps with their own workspaces on two streams do not disturb one another."""
+    blocks = [Block(300, 11), Block(300, 12)]
+    want = []
+    for b in blocks:
+        b.step()
+        torch.cuda.synchronize()
+        want.append([r.clone() for r in b.results()])
+        for r in b.results():
+            r.zero_()
+    streams = [torch.cuda.Stream() for _ in blocks]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for b, s in zip(blocks, streams):
+            with torch.cuda.stream(s):
+                b.step()
+    torch.cuda.synchronize()
+    for b, w in zip(blocks, want):
+        assert all(torch.equal(a, r) for a, r in zip(w, b.results()))
