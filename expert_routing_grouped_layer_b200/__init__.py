@@ -322,106 +322,46 @@ def moe_layer_forward_prenorm(cfg, x, T, norm_w, eps, weights, out, ws, dev_stat
            "moe_layer_forward_prenorm")
 
 
-# The operators below take tensors and read sizes, strides and types from them. The
-# tensors have to lie on one CUDA device, which is current during the call; without a
-# `stream` the call goes to that device's current stream. These checks run on every call,
-# so they are written for few Python operations (about 4 us a call, besides the launch).
-def _rows(name, t, dev, dtype, shape):
-    """(address, row stride) of a row-major matrix on device `dev` whose rows are dense."""
-    if t is None or t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
-        _refuse(name, t, dev, dtype, shape)
-    ld, step = t.stride()
-    rows, cols = shape
-    if rows <= 1 and ld < cols:  # the stride of a single row is never used
-        ld = cols
-    if ld < cols or (step != 1 and cols > 1):
-        raise ValueError("%s: strides %s; the elements of a row must be adjacent and rows must not overlap"
-                         % (name, t.stride()))
-    return t.data_ptr(), ld
+# The operators below take tensors; the native module next to this file (csrc/binding.cpp)
+# reads sizes, strides and types from them, checks them (ValueError) and calls the library.
+# The tensors have to lie on one CUDA device, which is current during the call; without a
+# `stream` the call goes to that device's current stream.
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
+_BOUND = ("moe_norm", "moe_norm_backward", "moe_route", "moe_route_backward", "moe_combine_backward",
+          "moe_linear", "moe_linear_backward")
+_binding = None
 
 
-def _vec(name, t, dev, dtype, shape):
-    """Address of a contiguous tensor on device `dev`, or None for None."""
-    if t is None:
-        return None
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
-        _refuse(name, t, dev, dtype, shape)
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+def _native():
+    """Load the native module and give it the library's functions (once)."""
+    global _binding
+    l = lib()
+    with _lock:
+        if _binding is None:
+            if not os.path.exists(BINDING_PATH):
+                raise RuntimeError("_binding.so is not built (expected at %s); run "
+                                   "`python -m expert_routing_grouped_layer_b200.build`" % BINDING_PATH)
+            import importlib.util
+
+            import torch  # noqa: F401 (its libraries have to be loaded first)
+            spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH)
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
+            m.bind(*(ctypes.cast(getattr(l, n), ctypes.c_void_p).value for n in _BOUND))
+            _binding = m
+    return _binding
 
 
-def _bytes(name, t, dev):
-    """(address, size in bytes) of a workspace on device `dev`; (None, 0) for None."""
-    if t is None:
-        return None, 0
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError("%s must be contiguous and on device %d" % (name, dev))
-    return t.data_ptr(), t.numel() * t.element_size()
-
-
-def _refuse(name, t, dev, dtype, shape):
-    if t is None:
-        raise ValueError("%s is missing" % name)
-    if t.get_device() != dev:
-        raise ValueError("%s is on %s, not on CUDA device %d" % (name, t.device, dev))
-    if t.dtype is not dtype:
-        raise ValueError("%s is %s, not %s" % (name, t.dtype, dtype))
-    raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
-
-
-def _matrix(name, t):
-    """(device index, MOE_T_* type, torch type, rows, columns, address, row stride) of a call's
-    first operand."""
-    if _torch is None:
-        _bind_torch()
-    d = _dtype_of.get(t.dtype)
-    if d is None:
-        raise ValueError("%s is %s: bfloat16, float16 or float32 is wanted" % (name, t.dtype))
-    dev = t.get_device()
-    if dev < 0 or not t.is_cuda:
-        raise ValueError("%s is not on a CUDA device" % name)
-    if t.dim() != 2:
-        raise ValueError("%s has shape %s: a matrix is wanted" % (name, tuple(t.shape)))
-    p, ld = _rows(name, t, dev, t.dtype, t.shape)
-    rows, cols = t.shape
-    return dev, d, t.dtype, rows, cols, p, ld
-
-
-_torch = None
-_dtype_of: dict = {}
-_f32 = _i32 = _bf16 = _current_device = _raw_stream = None
-
-
-def _bind_torch():
-    """Names of torch that every call needs, looked up once."""
-    global _torch, _f32, _i32, _bf16, _current_device, _raw_stream
-    import torch
-    _dtype_of.update({getattr(torch, n): v for n, v in DTYPE.items()})
-    _f32, _i32, _bf16 = torch.float32, torch.int32, torch.bfloat16
-    _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    _torch = torch
-
-
-def _call(fn, where, dev, stream, *args):
-    """fn(*args, stream) with device `dev` current."""
-    if dev == _current_device():
-        status = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
-    else:
-        with _torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
-    if status:
-        raise MoEError(status, where)
+def _handle(stream):
+    return None if stream is None else _stream(stream)
 
 
 def moe_norm(x, w, b, eps, y, mean=None, rstd=None, kind="layer", stream=None):
     """Layer norm (or RMS norm, kind="rms") of the rows of x [T, H] into y; w and b fp32
     [H] or None; mean and rstd fp32 [T] are filled where given."""
-    dev, dt, t, T, H, px, ldx = _matrix("x", x)
-    py, ldy = _rows("y", y, dev, t, (T, H))
-    _call(lib().moe_norm, "moe_norm", dev, stream, NORM_KIND[kind], dt, px, ldx, T, H,
-          _vec("w", w, dev, _f32, (H,)), _vec("b", b, dev, _f32, (H,)), eps, py, ldy,
-          _vec("mean", mean, dev, _f32, (T,)), _vec("rstd", rstd, dev, _f32, (T,)))
+    s = (_binding or _native()).norm(x, w, b, eps, y, mean, rstd, NORM_KIND[kind], _handle(stream))
+    if s:
+        raise MoEError(s, "moe_norm")
 
 
 def moe_norm_backward_workspace_bytes(T: int, H: int) -> int:
@@ -431,67 +371,48 @@ def moe_norm_backward_workspace_bytes(T: int, H: int) -> int:
 def moe_norm_backward(dy, x, w, mean, rstd, dx, dw, db, ws, kind="layer", stream=None):
     """Gradients of moe_norm: dx [T, H] like x, dw and db fp32 [H]; each may be None. ws: at
     least moe_norm_backward_workspace_bytes(T, H) bytes (None without dw and db)."""
-    dev, dt, t, T, H, px, ldx = _matrix("x", x)
-    pg, ldg = _rows("dy", dy, dev, t, (T, H))
-    pd, ldd = _rows("dx", dx, dev, t, (T, H)) if dx is not None else (None, H)
-    pws, nws = _bytes("ws", ws, dev)
-    _call(lib().moe_norm_backward, "moe_norm_backward", dev, stream, NORM_KIND[kind], dt, pg, ldg, px,
-          ldx, T, H, _vec("w", w, dev, _f32, (H,)), _vec("mean", mean, dev, _f32, (T,)),
-          _vec("rstd", rstd, dev, _f32, (T,)), pd, ldd, _vec("dw", dw, dev, _f32, (H,)),
-          _vec("db", db, dev, _f32, (H,)), pws, nws)
-
-
-def _router(cfg, logits):
-    c = _cfg(cfg)
-    dev, dt, t, T, E, p, ld = _matrix("logits", logits)
-    if E != c.n_routed_experts:
-        raise ValueError("logits has %d columns, not %d" % (E, c.n_routed_experts))
-    return c, dev, dt, t, T, c.num_experts_per_tok, E, p, ld
+    s = (_binding or _native()).norm_backward(dy, x, w, mean, rstd, dx, dw, db, ws, NORM_KIND[kind],
+                                              _handle(stream))
+    if s:
+        raise MoEError(s, "moe_norm_backward")
 
 
 def moe_route(cfg, logits, bias, topk_idx, topk_w, stream=None):
     """Experts and weights from router logits [T, E] (bf16, f16 or fp32) and a balance bias
     fp32 [E] or None: topk_idx int32 [T, k], topk_w fp32 [T, k]."""
-    c, dev, dt, t, T, k, E, p, ld = _router(cfg, logits)
-    _call(lib().moe_route, "moe_route", dev, stream, c, dt, p, ld, T, _vec("bias", bias, dev, _f32, (E,)),
-          _vec("topk_idx", topk_idx, dev, _i32, (T, k)), _vec("topk_w", topk_w, dev, _f32, (T, k)))
+    c = _cfg(cfg)
+    s = (_binding or _native()).route(ctypes.addressof(c), logits, bias, topk_idx, topk_w,
+                                      _handle(stream))
+    if s:
+        raise MoEError(s, "moe_route")
 
 
 def moe_route_backward(cfg, logits, topk_idx, dtopk_w, dlogits, stream=None):
     """dlogits [T, E], like logits, from the gradient dtopk_w fp32 [T, k] of moe_route's weights."""
-    c, dev, dt, t, T, k, E, p, ld = _router(cfg, logits)
-    pd, ldd = _rows("dlogits", dlogits, dev, t, (T, E))
-    _call(lib().moe_route_backward, "moe_route_backward", dev, stream, c, dt, p, ld, T,
-          _vec("topk_idx", topk_idx, dev, _i32, (T, k)), _vec("dtopk_w", dtopk_w, dev, _f32, (T, k)), pd,
-          ldd)
+    c = _cfg(cfg)
+    s = (_binding or _native()).route_backward(ctypes.addressof(c), logits, topk_idx, dtopk_w, dlogits,
+                                               _handle(stream))
+    if s:
+        raise MoEError(s, "moe_route_backward")
 
 
 def moe_combine_backward(cfg, dout, y, row_of, topk_w, dy, dtopk_w, stream=None):
     """Gradients of moe_combine: dy bf16 [N, H] (rows of dropped pairs stay as they are) and
     dtopk_w fp32 [T, k] (None: not wanted, y may then be None)."""
     c = _cfg(cfg)
-    dev, _, t, T, H, p, _ = _matrix("dout", dout)
-    k = c.num_experts_per_tok
-    n = (T * k, c.hidden)
-    _call(lib().moe_combine_backward, "moe_combine_backward", dev, stream, c,
-          _vec("dout", dout, dev, _bf16, (T, c.hidden)), _vec("y", y, dev, _bf16, n),
-          _vec("row_of", row_of, dev, _i32, (T * k,)), _vec("topk_w", topk_w, dev, _f32, (T, k)), T,
-          _vec("dy", dy, dev, _bf16, n), _vec("dtopk_w", dtopk_w, dev, _f32, (T, k)))
+    s = (_binding or _native()).combine_backward(ctypes.addressof(c), dout, y, row_of, topk_w, dy, dtopk_w,
+                                                 _handle(stream))
+    if s:
+        raise MoEError(s, "moe_combine_backward")
 
 
 def moe_linear(x, w, bias, residual, y, pre=None, act="none", dev_status=None, stream=None):
     """y [M, N] = act(x [M, K] w [N, K]^T + bias) + residual, bf16 or f16; bias fp32 [N] or None,
     residual [M, N] or None, pre [M, N] (None: not wanted) receives the value before act. Rows of
     x and w start on 16-byte boundaries (strides in multiples of 8 elements)."""
-    dev, dt, t, M, K, px, ldx = _matrix("x", x)
-    N = w.shape[0]
-    pw, ldw = _rows("w", w, dev, t, (N, K))
-    py, ldy = _rows("y", y, dev, t, (M, N))
-    pr, ldr = _rows("residual", residual, dev, t, (M, N)) if residual is not None else (None, N)
-    pp, ldp = _rows("pre", pre, dev, t, (M, N)) if pre is not None else (None, N)
-    _call(lib().moe_linear, "moe_linear", dev, stream, dt, px, ldx, pw, ldw,
-          _vec("bias", bias, dev, _f32, (N,)), pr, ldr, ACT[act], M, N, K, py, ldy, pp, ldp,
-          _vec("dev_status", dev_status, dev, _i32, (1,)))
+    s = (_binding or _native()).linear(x, w, bias, residual, y, pre, ACT[act], dev_status, _handle(stream))
+    if s:
+        raise MoEError(s, "moe_linear")
 
 
 def moe_linear_backward_workspace_bytes(M: int, N: int, K: int, act="none") -> int:
@@ -502,17 +423,10 @@ def moe_linear_backward(dy, x, w, pre, dx, dw, db, ws, act="none", dev_status=No
     """Gradients of moe_linear: dx like x, dw like w, db fp32 [N]; each may be None. pre as
     moe_linear wrote it (None for act="none"); the residual's gradient is dy. ws: at least
     moe_linear_backward_workspace_bytes(M, N, K, act) bytes."""
-    dev, dt, t, M, K, px, ldx = _matrix("x", x)
-    N = w.shape[0]
-    pw, ldw = _rows("w", w, dev, t, (N, K))
-    pg, ldg = _rows("dy", dy, dev, t, (M, N))
-    pp, ldp = _rows("pre", pre, dev, t, (M, N)) if pre is not None else (None, N)
-    pdx, lddx = _rows("dx", dx, dev, t, (M, K)) if dx is not None else (None, K)
-    pdw, lddw = _rows("dw", dw, dev, t, (N, K)) if dw is not None else (None, K)
-    pws, nws = _bytes("ws", ws, dev)
-    _call(lib().moe_linear_backward, "moe_linear_backward", dev, stream, dt, pg, ldg, px, ldx, pw, ldw, pp,
-          ldp, ACT[act], M, N, K, pdx, lddx, pdw, lddw, _vec("db", db, dev, _f32, (N,)), pws, nws,
-          _vec("dev_status", dev_status, dev, _i32, (1,)))
+    s = (_binding or _native()).linear_backward(dy, x, w, pre, dx, dw, db, ws, ACT[act], dev_status,
+                                                _handle(stream))
+    if s:
+        raise MoEError(s, "moe_linear_backward")
 
 
 class MoELayer:

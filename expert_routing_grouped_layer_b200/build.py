@@ -1,4 +1,5 @@
-"""Build libmoe.so (the CUDA library behind include/moe.h) in-tree for sm_100a.
+"""Build libmoe.so (the CUDA library behind include/moe.h) in-tree for sm_100a, and
+_binding.so (csrc/binding.cpp, the tensor arguments of the row operators).
 
     python -m expert_routing_grouped_layer_b200.build [--force] [--verbose]
 
@@ -17,6 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoe.so")
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -44,7 +47,33 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile the native module against the installed torch's headers (no nvcc)."""
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "moe.h")]
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    build_binding(force, verbose)
     if not force and not _stale():
         return LIB
     tmp = LIB + ".tmp%d" % os.getpid()

@@ -119,65 +119,86 @@ def test_linear_backward(lib):
     assert f(dx=None, dw=None, db=None) == OK
 
 
+F32, BF, I32 = torch.float32, torch.bfloat16, torch.int32
+
+
+def _refused(why, fn, *args, **kw):
+    with pytest.raises(ValueError, match=why):
+        fn(*args, **kw)
+
+
 def test_binding_refuses_before_the_library(lib):
-    """Tensors that are not on a GPU never reach a kernel; shapes, types and strides are
-    checked on the tensors themselves."""
-    x = torch.zeros(4, 64)
-    with pytest.raises(ValueError, match="not on a CUDA device"):
-        moe.moe_norm(x, None, None, 1e-6, x)
-    with pytest.raises(ValueError, match="not on a CUDA device"):
-        moe.moe_route(W.CONFIGS["tiny_bf16"], torch.zeros(4, 16), None, None, None)
-    with pytest.raises(ValueError, match="not on a CUDA device"):
-        moe.moe_combine_backward(W.CONFIGS["tiny_bf16"], torch.zeros(4, 256), None, None, None, None, None)
+    """The native module checks type, shape and layout, then the device: tensors on the CPU
+    pass every check but the last and never reach the library."""
+    z = torch.zeros
+    cfg = W.CONFIGS["tiny_bf16"]
+    E, k, H = cfg.n_routed_experts, cfg.num_experts_per_tok, cfg.hidden
+    x, w, t = z(4, 64, dtype=BF), z(64), z(4)
+    ws = z(64)
+    dev = "not on a CUDA device"
+    _refused(dev, moe.moe_norm, x, w, w, 1e-6, x, t, t)
+    _refused(dev, moe.moe_norm_backward, x, x, w, t, t, x, w, w, ws)
+    l, idx, tw = z(4, E), z(4, k, dtype=I32), z(4, k)
+    _refused(dev, moe.moe_route, cfg, l, z(E), idx, tw)
+    _refused(dev, moe.moe_route_backward, cfg, l, idx, tw, l)
+    d, y, ro = z(4, H, dtype=BF), z(4 * k, H, dtype=BF), z(4 * k, dtype=I32)
+    _refused(dev, moe.moe_combine_backward, cfg, d, y, ro, tw, y, tw)
+    wt, o = z(8, 64, dtype=BF), z(4, 8, dtype=BF)
+    _refused(dev, moe.moe_linear, x, wt, z(8), o, o, o)
+    _refused(dev, moe.moe_linear_backward, o, x, wt, o, x, wt, z(8), ws, act="relu")
 
 
-class _Fake:
-    """Stands for a device tensor in the binding's checks."""
-    is_cuda = True
-    device = "cuda:0"
+def test_binding_checks_layout(lib):
+    z = torch.zeros
+    x, w, t = z(4, 64, dtype=BF), z(64), z(4)
+    n = lambda x_=x, w_=w, b_=None, y_=x, m_=None, eps=1e-6, **kw: moe.moe_norm(x_, w_, b_, eps, y_, m_, t, **kw)
+    _refused("x is missing", n, x_=None)
+    _refused("not a tensor", n, x_=[1, 2])
+    _refused("a matrix", n, x_=z(64, dtype=BF))
+    _refused("float32 is wanted", n, x_=z(4, 64, dtype=torch.float64))
+    _refused("adjacent", n, x_=z(4, 128, dtype=BF)[:, ::2])
+    _refused("overlap", n, x_=z(64, dtype=BF).expand(4, 64))
+    _refused("overlap", n, y_=z(200, dtype=BF).as_strided((4, 64), (32, 1)))
+    _refused("y is missing", n, y_=None)
+    _refused(r"shape \(4, 65\), not \(4, 64\)", n, y_=z(4, 65, dtype=BF))
+    _refused("torch.float16, not torch.bfloat16", n, y_=z(4, 64, dtype=torch.float16))
+    _refused("w has shape", n, w_=z(63))
+    _refused("not torch.float32", n, w_=z(64, dtype=BF))
+    _refused("contiguous", n, w_=z(128)[::2])
+    _refused("mean has shape", n, m_=z(5))
+    _refused("strided", n, x_=x.to_sparse())
+    with pytest.raises(KeyError):
+        n(kind="batch")
+    with pytest.raises((ValueError, TypeError)):
+        n(eps="a")
+    with pytest.raises((ValueError, TypeError)):
+        n(eps=None)
+    # a single row's stride is not looked at
+    _refused("not on a CUDA device", moe.moe_norm, z(64, dtype=BF).as_strided((1, 64), (1, 1)), None, None, 1e-6,
+             z(1, 64, dtype=BF))
+    cfg = W.CONFIGS["tiny_bf16"]
+    E, k, H = cfg.n_routed_experts, cfg.num_experts_per_tok, cfg.hidden
+    idx, tw = z(4, k, dtype=I32), z(4, k)
+    _refused("logits has 17 columns", moe.moe_route, cfg, z(4, 17), None, idx, tw)
+    _refused("topk_idx is torch.float32", moe.moe_route, cfg, z(4, E), None, tw, tw)
+    _refused("topk_w has shape", moe.moe_route, cfg, z(4, E), None, idx, z(4, k + 1))
+    _refused("dlogits is torch.float32", moe.moe_route_backward, cfg, z(4, E, dtype=BF), idx, tw, z(4, E))
+    d, y, ro = z(4, H, dtype=BF), z(4 * k, H, dtype=BF), z(4 * k, dtype=I32)
+    _refused("dout has shape", moe.moe_combine_backward, cfg, z(4, H + 1, dtype=BF), y, ro, tw, y, tw)
+    _refused("y has shape", moe.moe_combine_backward, cfg, d, z(4, H, dtype=BF), ro, tw, y, tw)
+    _refused("contiguous", moe.moe_combine_backward, cfg, z(4, 2 * H, dtype=BF)[:, :H], y, ro, tw, y, tw)
+    xl, wt, o = z(4, 64, dtype=BF), z(8, 64, dtype=BF), z(4, 8, dtype=BF)
+    _refused("w has shape", moe.moe_linear, xl, z(8, 65, dtype=BF), None, None, o)
+    _refused("w is torch.float16", moe.moe_linear, xl, wt.half(), None, None, o)
+    _refused("residual has shape", moe.moe_linear, xl, wt, None, z(4, 9, dtype=BF), o)
+    _refused("bias is torch.bfloat16", moe.moe_linear, xl, wt, z(8, dtype=BF), None, o)
+    _refused("dw has shape", moe.moe_linear_backward, o, xl, wt, None, None, z(8, 63, dtype=BF), None, None)
+    with pytest.raises(KeyError):
+        moe.moe_linear(xl, wt, None, None, o, act="swish")
 
-    def __init__(self, shape, stride, dtype=torch.bfloat16, dev=0):
-        self.shape, self._s, self.dtype, self._d = shape, stride, dtype, dev
 
-    def dim(self):
-        return len(self.shape)
-
-    def stride(self):
-        return self._s
-
-    def get_device(self):
-        return self._d
-
-    def is_contiguous(self):
-        return False
-
-    def data_ptr(self):
-        return 4096
-
-
-def test_binding_checks_layout():
-    bf = torch.bfloat16
-    rows = lambda t, shape=(4, 64), dtype=bf: moe._rows("x", t, 0, dtype, shape)
-    assert rows(_Fake((4, 64), (72, 1))) == (4096, 72)
-    assert rows(_Fake((1, 64), (1, 1)), (1, 64)) == (4096, 64)
-    for t, why in [(_Fake((4, 64), (64, 2)), "adjacent"), (_Fake((4, 64), (32, 1)), "overlap"),
-                   (_Fake((4, 64), (0, 1)), "overlap"), (_Fake((4, 65), (65, 1)), "shape"),
-                   (_Fake((64,), (1,)), "shape"), (None, "is missing"),
-                   (_Fake((4, 64), (64, 1), dev=1), "not on CUDA device 0"),
-                   (_Fake((4, 64), (64, 1), torch.float16), "not torch.bfloat16")]:
-        with pytest.raises(ValueError, match=why):
-            rows(t)
-    with pytest.raises(ValueError, match="contiguous"):
-        moe._vec("w", _Fake((64,), (2,)), 0, bf, (64,))
-    with pytest.raises(ValueError, match="not torch.float32"):
-        moe._vec("w", _Fake((64,), (1,)), 0, torch.float32, (64,))
-    with pytest.raises(ValueError, match="contiguous"):
-        moe._bytes("ws", _Fake((64,), (2,)), 0)
-    assert moe._bytes("ws", None, 0) == (None, 0)
-    with pytest.raises(ValueError, match="float32 is wanted"):
-        moe._matrix("x", _Fake((4, 64), (64, 1), torch.float64))
-    with pytest.raises(ValueError, match="a matrix"):
-        moe._matrix("x", _Fake((64,), (1,)))
-    with pytest.raises(ValueError, match="adjacent"):
-        moe._matrix("x", _Fake((4, 64), (64, 2)))
-    assert moe._matrix("x", _Fake((4, 64), (72, 1))) == (0, 0, bf, 4, 64, 4096, 72)
+def test_missing_binding_fails_loudly(lib, monkeypatch, tmp_path):
+    monkeypatch.setattr(moe, "BINDING_PATH", str(tmp_path / "nope.so"))
+    monkeypatch.setattr(moe, "_binding", None)
+    with pytest.raises(RuntimeError, match="not built"):
+        moe.moe_norm(torch.zeros(4, 64), None, None, 1e-6, torch.zeros(4, 64))
