@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(kSplitThreads)
         mbar_init(gathered, 1);
         *abort_flag = 0;
         fence_barrier_init();
-        if (split > 1 && my_rows > 0) mbar_arrive_expect_tx(gathered, (uint32_t)(split * my_rows * 512));
+        if (split > 1 && my_rows > 0) mbar_arrive_expect_tx(gathered, (uint32_t)((split - 1) * my_rows * 512));
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
     }
@@ -823,13 +823,12 @@ __global__ void __launch_bounds__(kSplitThreads)
     tc_fence_before();
     const int col = c0 + lane * 4;
     const float4 b = bias4(epi, col);
-    const float* rows = part;  // of this CTA's first row; partial tiles of the peers RP rows apart
     bool ok = true;
     if (split > 1) {
         fence_proxy_async_smem();
         __syncthreads();
         cluster_wait();  // the peers' barriers are initialised
-        if (warp == 0 && lane < split) {
+        if (warp == 0 && lane < split && lane != rank) {
             const int n = max(0, min(RP, n_valid - lane * RP));
             if (n > 0)
                 copy_to_peer(gather + rank * RP * 128, gathered, lane, part + lane * RP * 128, (uint32_t)(n * 512));
@@ -838,7 +837,6 @@ __global__ void __launch_bounds__(kSplitThreads)
         if (!ok) status_or(d.status, MOE_DEV_TIMEOUT);
         __syncwarp();
         cluster_arrive_relaxed();  // the peers' copies to this CTA have landed
-        rows = gather;
     } else {
         __syncthreads();
     }
@@ -851,13 +849,14 @@ __global__ void __launch_bounds__(kSplitThreads)
         for (int i = 0; i < U; ++i) {
             const int ri = min(r + 8 * i, my_rows - 1);
             if (epi.res && quad_at(epi, col)) res[i] = res4<T>(epi, r0 + rank * RP + ri, col);
-            a[i] = *reinterpret_cast<const float4*>(rows + ri * 128 + lane * 4);
+            a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        for (int p = 1; p < split; ++p) {
+        for (int p = 0; p < split; ++p) {  // in rank order, this CTA's own partial tile in its turn
+            const float* rows = p == rank ? part + rank * RP * 128 : gather + p * RP * 128;
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int ri = min(r + 8 * i, my_rows - 1);
-                const float4 v = *reinterpret_cast<const float4*>(rows + (p * RP + ri) * 128 + lane * 4);
+                const float4 v = *reinterpret_cast<const float4*>(rows + ri * 128 + lane * 4);
                 a[i].x += v.x; a[i].y += v.y; a[i].z += v.z; a[i].w += v.w;
             }
         }
