@@ -16,6 +16,7 @@
 // One warp per token holds the row in registers. The cost is the exponentials and the
 // k rounds of a warp-wide maximum (redux.sync on order-preserving integer keys), not
 // the bytes.
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -240,13 +241,13 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
     pdl_trigger();
     constexpr int J = NI * VEC;
     typedef unsigned long long u64;
-    __shared__ int list[8][32];
+    __shared__ int2 list[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long t = (long)blockIdx.x * (blockDim.x >> 5) + warp;
     if (t >= p.T) return;
     const T* row = static_cast<const T*>(p.logits) + t * p.ld;
     const int gsz = p.E / p.n_group;
-    const int g = lane / L, sub = lane - g * L;
+    const int shift = __ffs(L) - 1, g = lane >> shift, sub = lane & (L - 1);
     const int nvec = g < p.n_group ? gsz / VEC : 0;
     const int e0 = g * gsz + sub * VEC;  // element (i, v) is e0 + i L VEC + v
 
@@ -309,11 +310,14 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
         }
         return;
     }
-    // |computed s' - s'| <= eps * max(scale, |s'|): a few units of 2^-24 for the sigmoid and
-    // sqrt-softplus, up to J + 5 more for the softmax's sum
-    const float eps = p.score_fn == MOE_SCORE_SOFTMAX ? 9.6e-6f : 6.0e-7f;
+    // |computed s' - s'| <= err + 1.2e-7 |s'|: the last addition's rounding, and an error in
+    // proportion to the row's largest score: a few units of 2^-24, for the softmax also its
+    // sum's J + 5 additions
+    const float err = p.score_fn == MOE_SCORE_SOFTMAX ? (J + 24) * 6.0e-8f * (z > 0.f ? 1.0f / z : 0.f)
+                                                      : 4.8e-7f * scale;
+    auto bound = [&](float v) { return err + 1.2e-7f * fabsf(v); };
 
-    uint32_t kept = kFull;
+    bool keep = true;  // this lane's group is kept
     if (p.n_group > 1) {
         float b1 = -kInf, b2 = -kInf;
 #pragma unroll
@@ -327,21 +331,25 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
             b1 = fmaxf(b1, o1);
         }
         const float gs = b2 == -kInf ? b1 : b1 + b2;
-        int rank = 0;
-        for (int h = 0; h < p.n_group; ++h) {
-            const float o = __shfl_sync(kFull, gs, h * L);
-            rank += (o > gs || (o == gs && h < g)) ? 1 : 0;
-        }
         const bool real = g < p.n_group;
-        bool keep = real && rank < p.topk_group;
-        const float lo = -warp_max(keep ? -gs : -kInf);          // smallest kept
-        const float hi = warp_max(real && !keep ? gs : -kInf);   // largest left out
+        keep = false;
+        uint32_t gk = real ? key_of(gs) : 0u, lo_key = 0u;
+        for (int r = 0; r < p.topk_group; ++r) {  // the lower group of equal ones
+            lo_key = __reduce_max_sync(kFull, gk);
+            if (g == (__ffs(__ballot_sync(kFull, gk == lo_key)) - 1) >> shift) {
+                keep = true;
+                gk = 0u;
+            }
+        }
+        const uint32_t hi_key = __reduce_max_sync(kFull, gk);
+        const float lo = value_of(lo_key);                       // smallest kept
+        const float hi = hi_key ? value_of(hi_key) : -kInf;      // largest left out
         const float mag = warp_max(real && b1 != -kInf ? fmaxf(fabsf(b1), b2 == -kInf ? 0.f : fabsf(b2)) : 0.f);
-        const float tol = 5.f * eps * fmaxf(scale, mag);  // two sums of two values each
+        const float tol = 5.f * bound(mag);  // two sums of two values each
         if (hi != -kInf && !(lo - hi > tol)) {
             const double zd = p.score_fn == MOE_SCORE_SOFTMAX ? row_z<T>(row, p.E, m) : 1.0;
-            kept = groups_exact<T>(Row<T>{row, p.bias, p.E, gsz, p.score_fn, m, zd, kFull}, p.n_group,
-                                   p.topk_group);
+            const uint32_t kept = groups_exact<T>(Row<T>{row, p.bias, p.E, gsz, p.score_fn, m, zd, kFull},
+                                                  p.n_group, p.topk_group);
             keep = real && ((kept >> g) & 1u);
         }
         if (!keep) {
@@ -350,97 +358,136 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
         }
     }
 
-    // Each lane caches its two best elements; a round is one warp maximum over the
-    // lanes' heads. The winner pops its head and rescans when its cache is empty.
-    // Within a lane the expert grows with j, so the first of equal keys is the lower.
+    // The k-th largest of the lanes' maxima is a lower bound of the k-th largest of all. What
+    // is not below it (less the error bound) is a candidate: usually k to 2 k elements, one
+    // to a lane, of which k rounds of a warp maximum take the chosen in order.
     typedef typename std::conditional<(J > 32), u64, uint32_t>::type Bits;
+    auto expert = [&](int j) { return e0 + (j / VEC) * L * VEC + j % VEC; };
+    float v1 = sel[0];
+#pragma unroll
+    for (int j = 1; j < J; ++j) v1 = fmaxf(v1, sel[j]);
+    uint32_t lane_key = v1 == -kInf ? 0u : key_of(v1), tau = 0u;
+    for (int got = 0; got < p.k;) {
+        tau = __reduce_max_sync(kFull, lane_key);
+        if (tau == 0u) break;  // fewer lanes with elements than k: every element is a candidate
+        got += __popc(__ballot_sync(kFull, lane_key == tau));
+        if (lane_key == tau) lane_key = 0u;
+    }
+    float least = -FLT_MAX;
+    if (tau != 0u) {
+        least = value_of(tau);
+        if (!by_logit) least -= 2.f * bound(least);
+    }
     Bits avail = 0;
 #pragma unroll
     for (int j = 0; j < J; ++j)
-        if (sel[j] != -kInf) avail |= Bits(1) << j;
-    auto expert = [&](int j) { return e0 + (j / VEC) * L * VEC + j % VEC; };
-    uint32_t k1, k2;
-    int e1, e2;
-    Bits bit1, bit2;
-    auto refill = [&]() {
-        float v1 = -kInf, v2 = -kInf;
-        e1 = e2 = INT_MAX;
-        bit1 = bit2 = 0;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const float v = avail & (Bits(1) << j) ? sel[j] : -kInf;
-            const bool first = v > v1, second = v > v2;
-            v2 = first ? v1 : (second ? v : v2);
-            e2 = first ? e1 : (second ? expert(j) : e2);
-            bit2 = first ? bit1 : (second ? Bits(1) << j : bit2);
-            v1 = first ? v : v1;
-            e1 = first ? expert(j) : e1;
-            bit1 = first ? Bits(1) << j : bit1;
-        }
-        k1 = bit1 ? key_of(v1) : 0u;
-        k2 = bit2 ? key_of(v2) : 0u;
-    };
-    refill();
+        if (sel[j] >= least) avail |= Bits(1) << j;
+    const int mine = J > 32 ? __popcll(avail) : __popc((uint32_t)avail);
+    const int total = __reduce_add_sync(kFull, mine);
+
     int my_e = -1;
     uint32_t my_key = 0u, last = 0u;
-    for (int r = 0; r < p.k; ++r) {
-        const uint32_t top = __reduce_max_sync(kFull, k1);
-        if (top == 0u) break;  // fewer than k experts are left
-        const uint32_t who = __ballot_sync(kFull, k1 == top);
-        int e = __shfl_sync(kFull, e1, __ffs(who) - 1);
-        if (who & (who - 1)) e = __reduce_min_sync(kFull, k1 == top ? e1 : INT_MAX);  // the lowest index
+    auto take = [&](int r, uint32_t key, int e) {  // round r: the largest key, the lowest index among equals
+        last = __reduce_max_sync(kFull, key);
+        const uint32_t who = __ballot_sync(kFull, key == last);
+        int win = __shfl_sync(kFull, e, __ffs(who) - 1);
+        if (who & (who - 1)) win = __reduce_min_sync(kFull, key == last ? e : INT_MAX);
         if (lane == r) {
-            my_e = e;
-            my_key = top;
+            my_e = win;
+            my_key = last;
         }
-        last = top;
-        if (e1 == e) {
-            avail &= ~bit1;
-            k1 = k2; e1 = e2; bit1 = bit2;
-            k2 = 0u; e2 = INT_MAX; bit2 = 0;
-            if (k1 == 0u && avail) refill();
-        }
-    }
-    const float my_l0 = my_e >= 0 ? to_f32<T>(row[my_e]) + 0.0f : 0.f;
-    float my_l = my_l0;
-    if (!by_logit && last != 0u) {
-        // values that the bound cannot tell apart and that are not the same number: among
-        // the chosen one after the other, and of those left out against the last chosen
-        const float mine = value_of(my_key);
-        const float my_b = my_e >= 0 && p.bias ? p.bias[my_e] : 0.f;
-        const uint32_t next_key = __shfl_down_sync(kFull, my_key, 1);
-        const float next_l = __shfl_down_sync(kFull, my_l0, 1), next_b = __shfl_down_sync(kFull, my_b, 1);
-        const float tol = 2.f * eps * fmaxf(scale, fabsf(mine));
-        bool near = lane + 1 < p.k && next_key != 0u && mine - value_of(next_key) <= tol &&
-                    !(next_l == my_l0 && next_b == my_b);
-        const int chosen = __popc(__ballot_sync(kFull, my_e >= 0));
-        const float last_v = value_of(last);
-        const float cut = last_v - 2.f * eps * fmaxf(scale, fabsf(last_v));
-        const float ll = __shfl_sync(kFull, my_l0, chosen - 1), lb = __shfl_sync(kFull, my_b, chosen - 1);
-        if (k1 != 0u && value_of(k1) >= cut) {
+        return win;
+    };
+    const bool listed = total <= 32;
+    uint32_t k1 = 0u;  // largest key of this lane that is not chosen
+    int e1 = INT_MAX;
+    if (listed) {
+        int at = mine;
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-                if ((avail & (Bits(1) << j)) && sel[j] >= cut) {
-                    const int e = expert(j);
-                    near |= !(to_f32<T>(row[e]) + 0.0f == ll && (p.bias ? p.bias[e] : 0.f) == lb);
-                }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(kFull, at, o);
+            if (lane >= o) at += n;
         }
-        if (__any_sync(kFull, near)) {
-            // candidates: everything chosen or not below the cut
-            int count = 0;
+        at -= mine;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (avail & (Bits(1) << j)) list[warp][at++] = make_int2(__float_as_int(sel[j]), expert(j));
+        __syncwarp();
+        if (lane < total) {
+            const int2 c = list[warp][lane];
+            k1 = key_of(__int_as_float(c.x));
+            e1 = c.y;
+        }
+        for (int r = 0; r < min(p.k, total); ++r)
+            if (take(r, k1, e1) == e1) k1 = 0u;
+    } else {
+        // rows of equal scores, or few lanes with many elements each: a lane caches its two
+        // best and scans again when both are taken. Within a lane the expert grows with j,
+        // so the first of equal values is the lower.
+        uint32_t k2;
+        int e2;
+        Bits bit1, bit2;
+        auto refill = [&]() {
+            float f1 = -kInf, f2 = -kInf;
+            e1 = e2 = INT_MAX;
+            bit1 = bit2 = 0;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const bool in = sel[j] >= cut;
-                const uint32_t who = __ballot_sync(kFull, in);
-                const int at = count + __popc(who & ((1u << lane) - 1));
-                if (in && at < 32) list[warp][at] = expert(j);
-                count += __popc(who);
+                const float v = avail & (Bits(1) << j) ? sel[j] : -kInf;
+                const bool first = v > f1, second = v > f2;
+                f2 = first ? f1 : (second ? v : f2);
+                e2 = first ? e1 : (second ? expert(j) : e2);
+                bit2 = first ? bit1 : (second ? Bits(1) << j : bit2);
+                f1 = first ? v : f1;
+                e1 = first ? expert(j) : e1;
+                bit1 = first ? Bits(1) << j : bit1;
             }
-            __syncwarp();
+            k1 = bit1 ? key_of(f1) : 0u;
+            k2 = bit2 ? key_of(f2) : 0u;
+        };
+        refill();
+        for (int r = 0; r < p.k; ++r) {  // total > 32 >= k: there is always one left
+            if (take(r, k1, e1) == e1) {
+                avail &= ~bit1;
+                k1 = k2; e1 = e2; bit1 = bit2;
+                k2 = 0u; e2 = INT_MAX; bit2 = 0;
+                if (k1 == 0u && avail) refill();
+            }
+        }
+    }
+    float my_l = my_e >= 0 ? to_f32<T>(row[my_e]) + 0.0f : 0.f;
+    if (!by_logit && total > 0) {
+        // values that the bound cannot tell apart and that are not the same number: among
+        // the chosen one after the other, and of those left out against the last chosen
+        const float my_v = value_of(my_key);
+        const float my_b = my_e >= 0 && p.bias ? p.bias[my_e] : 0.f;
+        const uint32_t next_key = __shfl_down_sync(kFull, my_key, 1);
+        const float next_l = __shfl_down_sync(kFull, my_l, 1), next_b = __shfl_down_sync(kFull, my_b, 1);
+        bool near = lane + 1 < p.k && next_key != 0u && my_v - value_of(next_key) <= 2.f * bound(my_v) &&
+                    !(next_l == my_l && next_b == my_b);
+        const int chosen = min(p.k, total);
+        const float last_v = value_of(last), cut = last_v - 2.f * bound(last_v);
+        const float ll = __shfl_sync(kFull, my_l, chosen - 1), lb = __shfl_sync(kFull, my_b, chosen - 1);
+        auto as_last = [&](int e) {
+            return to_f32<T>(row[e]) + 0.0f == ll && (p.bias ? p.bias[e] : 0.f) == lb;
+        };
+        if (k1 != 0u && value_of(k1) >= cut) {
+            if (listed) {
+                near |= !as_last(e1);
+            } else {
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    if ((avail & (Bits(1) << j)) && sel[j] >= cut) near |= !as_last(expert(j));
+            }
+        }
+        if (__any_sync(kFull, near)) {
             const double zd = p.score_fn == MOE_SCORE_SOFTMAX ? row_z<T>(row, p.E, m) : 1.0;
-            const Row<T> r{row, p.bias, p.E, gsz, p.score_fn, m, zd, p.n_group > 1 ? kept : kFull};
-            if (count <= 32) {
-                my_e = rank_exact<T>(r, lane < count ? list[warp][lane] : -1, count);
+            const uint32_t lanes = __ballot_sync(kFull, keep);
+            uint32_t kept = 0u;
+            for (int h = 0; h < p.n_group; ++h) kept |= ((lanes >> (h << shift)) & 1u) << h;
+            const Row<T> r{row, p.bias, p.E, gsz, p.score_fn, m, zd, kept};
+            if (listed) {
+                my_e = rank_exact<T>(r, lane < total ? list[warp][lane].y : -1, total);
                 if (lane >= p.k) my_e = -1;
             } else {
                 my_e = topk_exact<T>(r, p.k);

@@ -106,6 +106,39 @@ def test_a_left_out_expert_that_fp32_would_rank_behind():
             _check(cfg, l, b2)
 
 
+@pytest.mark.parametrize("E", [64, 256, 1024])
+def test_near_ties_inside_kept_groups(E):
+    """Two of four groups are clearly the best, with more nearly equal scores than lanes; the
+    others hold the best single expert, which no tie may bring back."""
+    l = torch.full((12, 4, E // 4), -5.0, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(E)
+    l[:, 0::2] = 1.0 + 2.0 ** -23 * torch.randint(0, 9, (12, 2, E // 4), generator=g, device="cuda")
+    l[:, 1::2, 3] = 2.0
+    l[6:, 0, 5:] = -5.0  # and fewer near ties than lanes
+    l[6:, 2, 5:] = -4.0
+    bias = 0.01 + 2.0 ** -30 * torch.randint(0, 4, (E,), generator=g, device="cuda")
+    for score in ("sigmoid", "sqrtsoftplus"):
+        idx = _check(_cfg(E, 8, 4, 2, score), l.view(12, E), bias)
+        assert (idx // (E // 4) % 2 == 0).all()
+        _check(_cfg(E, 8, 4, 2, score), l.view(12, E), None)
+
+
+def test_equal_logits():
+    """An untrained router: all logits equal, with and without a bias of zeros."""
+    for E, k, groups, kept in [(16, 4, 1, 1), (384, 8, 1, 1), (384, 8, 8, 4), (1024, 32, 16, 1)]:
+        for dt in (FL, BF):
+            l = torch.full((9, E), 0.25, dtype=dt, device="cuda")
+            for b in (None, torch.zeros(E, device="cuda")):
+                _check(_cfg(E, k, groups, kept), l, b)
+
+
+@pytest.mark.parametrize("groups,kept,E,k", [(16, 1, 1024, 30), (8, 1, 512, 8), (2, 1, 600, 32), (32, 2, 1024, 17)])
+def test_few_lanes_hold_all_candidates(groups, kept, E, k):
+    l, bias = _logits(40, E, FL, E + groups)
+    _check(_cfg(E, k, groups, kept), l, bias)
+    _check(_cfg(E, k, groups, kept, "softmax"), l, None)
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "sqrtsoftplus", "softmax"])
 @pytest.mark.parametrize("groups,kept", [(1, 1), (8, 2)])
 def test_masks(score, groups, kept):
