@@ -378,12 +378,31 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
         least = value_of(tau);
         if (!by_logit) least -= 2.f * bound(least);
     }
-    Bits avail = 0;
+    // the elements not below `from`, as bits and (up to 32 of them) in the warp's list
+    Bits avail;
+    auto collect = [&](float from) {
+        avail = 0;
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-        if (sel[j] >= least) avail |= Bits(1) << j;
-    const int mine = J > 32 ? __popcll(avail) : __popc((uint32_t)avail);
-    const int total = __reduce_add_sync(kFull, mine);
+        for (int j = 0; j < J; ++j)
+            if (sel[j] >= from) avail |= Bits(1) << j;
+        const int mine = J > 32 ? __popcll(avail) : __popc((uint32_t)avail);
+        int at = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(kFull, at, o);
+            if (lane >= o) at += n;
+        }
+        const int total = __shfl_sync(kFull, at, 31);
+        if (total <= 32) {
+            at -= mine;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (avail & (Bits(1) << j)) list[warp][at++] = make_int2(__float_as_int(sel[j]), expert(j));
+        }
+        __syncwarp();
+        return total;
+    };
+    const int total = collect(least);
 
     int my_e = -1;
     uint32_t my_key = 0u, last = 0u;
@@ -402,17 +421,6 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
     uint32_t k1 = 0u;  // largest key of this lane that is not chosen
     int e1 = INT_MAX;
     if (listed) {
-        int at = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int n = __shfl_up_sync(kFull, at, o);
-            if (lane >= o) at += n;
-        }
-        at -= mine;
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-            if (avail & (Bits(1) << j)) list[warp][at++] = make_int2(__float_as_int(sel[j]), expert(j));
-        __syncwarp();
         if (lane < total) {
             const int2 c = list[warp][lane];
             k1 = key_of(__int_as_float(c.x));
@@ -486,8 +494,9 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
             uint32_t kept = 0u;
             for (int h = 0; h < p.n_group; ++h) kept |= ((lanes >> (h << shift)) & 1u) << h;
             const Row<T> r{row, p.bias, p.E, gsz, p.score_fn, m, zd, kept};
-            if (listed) {
-                my_e = rank_exact<T>(r, lane < total ? list[warp][lane].y : -1, total);
+            const int close = listed ? total : collect(cut);
+            if (close <= 32) {
+                my_e = rank_exact<T>(r, lane < close ? list[warp][lane].y : -1, close);
                 if (lane >= p.k) my_e = -1;
             } else {
                 my_e = topk_exact<T>(r, p.k);
