@@ -117,32 +117,34 @@ __device__ __noinline__ double row_z(const T* l, int E, float m) {
     return warp_sum(z);
 }
 
-// The kept groups by their scores in double precision.
+// The kept groups by their scores in double precision: each group's L = 1 << shift lanes share
+// its elements, as in the fp32 path.
 template <typename T>
-__device__ __noinline__ uint32_t groups_exact(Row<T> r, int n_group, int topk_group) {
-    const int lane = threadIdx.x & 31;
-    double gs = -(double)kInf;
-    for (int g = 0; g < n_group; ++g) {
-        double b1 = -(double)kInf, b2 = b1;
-        for (int e = g * r.gsz + lane; e < (g + 1) * r.gsz; e += 32) {
+__device__ __noinline__ uint32_t groups_exact(Row<T> r, int n_group, int topk_group, int shift) {
+    const int lane = threadIdx.x & 31, g = lane >> shift, L = 1 << shift;
+    double b1 = -(double)kInf, b2 = b1;
+    if (g < n_group) {
+        for (int e = g * r.gsz + (lane & (L - 1)); e < (g + 1) * r.gsz; e += L) {
             const double v = r.sel(e, r.logit(e));
-            if (v > b1) { b2 = b1; b1 = v; }
-            else if (v > b2) b2 = v;
+            b2 = fmax(b2, fmin(b1, v));
+            b1 = fmax(b1, v);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const double o1 = __shfl_xor_sync(kFull, b1, o), o2 = __shfl_xor_sync(kFull, b2, o);
-            b2 = fmax(fmin(b1, o1), fmax(b2, o2));
-            b1 = fmax(b1, o1);
-        }
-        if (lane == g) gs = b2 == -(double)kInf ? b1 : b1 + b2;
     }
+    for (int o = L >> 1; o > 0; o >>= 1) {
+        const double o1 = __shfl_xor_sync(kFull, b1, o), o2 = __shfl_xor_sync(kFull, b2, o);
+        b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+        b1 = fmax(b1, o1);
+    }
+    const double gs = b2 == -(double)kInf ? b1 : b1 + b2;
     int rank = 0;
-    for (int g = 0; g < n_group; ++g) {
-        const double o = __shfl_sync(kFull, gs, g);
-        rank += (o > gs || (o == gs && g < lane)) ? 1 : 0;
+    for (int h = 0; h < n_group; ++h) {
+        const double o = __shfl_sync(kFull, gs, h << shift);
+        rank += (o > gs || (o == gs && h < g)) ? 1 : 0;
     }
-    return __ballot_sync(kFull, lane < n_group && rank < topk_group);
+    const uint32_t lanes = __ballot_sync(kFull, g < n_group && rank < topk_group);
+    uint32_t kept = 0u;
+    for (int h = 0; h < n_group; ++h) kept |= ((lanes >> (h << shift)) & 1u) << h;
+    return kept;
 }
 
 __device__ __forceinline__ bool better_d(double va, float la, int ia, double vb, float lb, int ib) {
@@ -236,7 +238,7 @@ __device__ __forceinline__ void load_bias(float* b, const float* p) {
 // a group's two largest come from the lanes of that group alone, and without groups
 // (L = 32) a load instruction covers consecutive elements.
 template <typename T, int VEC, int NI>
-__global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
+__global__ void __launch_bounds__(256, NI * VEC > 32 ? 1 : 3) route_fwd_kernel(RouteParams p, int L) {
     pdl_wait();
     pdl_trigger();
     constexpr int J = NI * VEC;
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(RouteParams p, int L) {
         if (hi != -kInf && !(lo - hi > tol)) {
             const double zd = p.score_fn == MOE_SCORE_SOFTMAX ? row_z<T>(row, p.E, m) : 1.0;
             const uint32_t kept = groups_exact<T>(Row<T>{row, p.bias, p.E, gsz, p.score_fn, m, zd, kFull},
-                                                  p.n_group, p.topk_group);
+                                                  p.n_group, p.topk_group, shift);
             keep = real && ((kept >> g) & 1u);
         }
         if (!keep) {
