@@ -5,6 +5,9 @@ function here only marshals arguments -- device pointers, sizes, the CUDA
 stream -- and calls the library of the same name; all arithmetic runs in the
 library's CUDA kernels. PyTorch provides device memory and streams only.
 
+The operators around the experts (moe_norm, moe_route, moe_combine_backward, moe_linear
+and their gradients) take tensors, which the native module _binding.so reads and checks.
+
 There is no fallback: if ``libmoe.so`` is missing, or no CUDA device is
 present, every call raises. Build the library with
 ``python -m expert_routing_grouped_layer_b200.build``.

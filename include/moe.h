@@ -408,7 +408,7 @@ moe_status moe_route_backward(const moe_config *cfg, int32_t dtype, const void *
  *  dy[row_of[t*k+j]] = bf16(topk_w[t][j] * dout[t])   (bf16 [N][H]),
  *  dtopk_w[t][j] = sum_h dout[t][h] * y[row_of[t*k+j]][h]   (fp32 [T][k]).
  *  A pair whose row is outside [0, N) has dtopk_w 0; rows of dy that no pair names are
- *  left as they are. The gradient of each shared expert's output is dout itself.
+ *  left as they are; the other pairs' rows are distinct (as moe_permute gives them). The gradient of each shared expert's output is dout itself.
  *  dtopk_w may be NULL (y is then not read and may be NULL). dy must not overlap dout
  *  or y. dout, y, dy 16-byte aligned. */
 moe_status moe_combine_backward(const moe_config *cfg, const void *dout, const void *y,

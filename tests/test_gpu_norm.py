@@ -138,6 +138,39 @@ def test_in_place_and_partial_outputs():
     assert (dw == 0).all() and (db == 0).all()
 
 
+@pytest.mark.parametrize("T,H", [(400, 1023), (30, 515), (64, 4097)])
+def test_in_place_off_the_16_byte_grid(T, H):
+    x, dy, w, b = _case(T, H, torch.bfloat16, 9)
+    y, mean, rstd = torch.empty_like(x), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    moe.moe_norm(x, w, b, 1e-6, y, mean, rstd)
+    dx = torch.empty_like(x)
+    moe.moe_norm_backward(dy, x, w, mean, rstd, dx, None, None, None)
+    for _ in range(5):
+        z = x.clone()
+        moe.moe_norm(z, w, b, 1e-6, z)
+        assert torch.equal(z, y)
+        for keep in (dy, x):
+            g = keep.clone()
+            moe.moe_norm_backward(g if keep is dy else dy, g if keep is x else x, w, mean, rstd, g, None, None, None)
+            assert torch.equal(g, dx)
+
+
+def test_rows_between_other_data():
+    """NaN before, between and behind the rows reaches nothing, on and off the 16-byte grid."""
+    for off, H, ld in [(0, 120, 128), (1, 120, 131), (3, 119, 129)]:
+        T = 700
+        g = torch.Generator(device="cuda").manual_seed(H)
+        flat = torch.full((T * ld + 64,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        x = flat[off:off + T * ld].view(T, ld)[:, :H]
+        x.copy_(torch.randn(T, H, generator=g, device="cuda"))
+        _check(x, x.clone(), None, None, 1e-6, "layer")
+        y = torch.full_like(flat, 5.0)
+        moe.moe_norm(x, None, None, 1e-6, y[off:off + T * ld].view(T, ld)[:, :H])
+        mask = torch.ones_like(flat, dtype=torch.bool)
+        mask[off:off + T * ld].view(T, ld)[:, :H] = False
+        assert (y[mask] == 5).all() and torch.isfinite(y).all()
+
+
 def test_gradient_against_differences():
     x, _, w, b = _case(4, 96, torch.float32, 9)
     T, H = x.shape
