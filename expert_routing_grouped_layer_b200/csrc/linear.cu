@@ -252,12 +252,14 @@ struct GemmDims {
 // at K = 2048 and held the tensor cores up.
 struct PairCfg {
     static constexpr int A_BYTES = 128 * BK * 2;
-    static constexpr int RING_BYTES = 6 * 2 * A_BYTES;  // six stages of a 256-column tile, more of a narrower one
+    // the ring of stages (six of a 256-column tile, more of a narrower one) and the epilogue's
+    // blocks, three a warp with `pre` and two without
+    static constexpr int DATA_BYTES = 224 * 1024;
     static constexpr int MAX_STAGES = 9;
     static constexpr int EPI_WARPS = 8;
-    static constexpr int EPI_BYTES = EPI_WARPS * 4096;
+    static constexpr int epi_warp_bytes(bool pre) { return pre ? 3 * 2048 : 2 * 2048; }
     static constexpr int THREADS = 32 * (2 + EPI_WARPS);
-    static constexpr int SMEM_BYTES = 1024 + RING_BYTES + EPI_BYTES + 8 * (2 * MAX_STAGES + 5 + 2 * EPI_WARPS) + 16;
+    static constexpr int SMEM_BYTES = 1024 + DATA_BYTES + 8 * (2 * MAX_STAGES + 5 + 2 * EPI_WARPS) + 16;
     static_assert(SMEM_BYTES <= kSmemMax, "shared memory budget");
 };
 
@@ -297,14 +299,16 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t* stage_out = smem + C::RING_BYTES;
-    uint64_t* full = reinterpret_cast<uint64_t*>(stage_out + C::EPI_BYTES);
+    const int epi_warp = C::epi_warp_bytes(epi.pre != nullptr);
+    const int ring_bytes = C::DATA_BYTES - C::EPI_WARPS * epi_warp;
+    uint8_t* stage_out = smem + ring_bytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::DATA_BYTES);
     uint64_t* empty = full + C::MAX_STAGES;
     uint64_t* tfull = empty + C::MAX_STAGES;
     const int half = BN / 2;
     const int b_boxes = B_MN ? (half + 63) / 64 : 1;
     const int stage_bytes = C::A_BYTES + (B_MN ? b_boxes * 8192 : half * BK * 2);
-    const int stages = min(C::MAX_STAGES, C::RING_BYTES / stage_bytes);
+    const int stages = min(C::MAX_STAGES, ring_bytes / stage_bytes);
     uint64_t* tempty = tfull + 2;
     uint64_t* mma_done = tempty + 2;
     uint64_t* res_full = mma_done + 1;  // two per epilogue warp: a residual block is in
@@ -436,10 +440,9 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     } else {
         const int q = warp & 3, grp = (warp - 2) >> 2;
         if constexpr (TMA_OUT) {
-            // Buffers of 2 KB: with `pre`, 0 for the result (and residual) and 1 for pre; without,
-            // both alternate for the result, and the next chunk's residual is fetched into the
-            // other one while a chunk is worked on.
-            uint8_t* bufs = stage_out + (warp - 2) * 4096;
+            // Blocks of 2 KB: 0 and 1 alternate for the result, and the next chunk's residual is
+            // fetched into the other one while a chunk is worked on; 2 holds pre.
+            uint8_t* bufs = stage_out + (warp - 2) * epi_warp;
             uint64_t* res_bar = &res_full[2 * (warp - 2)];  // of buffer 0 and 1
             const bool has_pre = epi.pre != nullptr, has_res = epi.res != nullptr;
             const int y0 = (int)rank * 128 + q * 32;
@@ -466,9 +469,8 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
             };
             int nu = pair, nc = grp - 2;
             advance(nu, nc);  // the first chunk
-            const bool early = has_res && !has_pre;
             int fetched = 0;
-            if (early && lane == 0 && nu < total) {
+            if (has_res && lane == 0 && nu < total) {
                 fetch(nu, nc, 0);
                 ++fetched;
             }
@@ -483,15 +485,8 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                 const int row = tm * 256 + y0;
                 for (int c = grp; c < chunks; c += 2, ++n) {
                     const int col = tn * BN + c * 32;
-                    const int bi = has_pre ? 0 : n & 1;
+                    const int bi = n & 1;
                     uint8_t* buf = bufs + bi * 2048;
-                    if (has_pre && lane == 0) {
-                        bulk_wait_read<0>();  // the last chunk's blocks have left
-                        if (has_res) {
-                            fetch(u, c, 0);
-                            ++fetched;
-                        }
-                    }
                     uint32_t r0[16], r1[16];
                     tmem_ld16(taddr + c * 32, r0);
                     tmem_ld16(taddr + c * 32 + 16, r1);
@@ -507,16 +502,15 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                         z[j] += __uint_as_float(r0[j]);
                         z[j + 16] += __uint_as_float(r1[j]);
                     }
-                    if (!has_pre && lane == 0) {
-                        if (early) {
-                            bulk_wait_read<0>();  // the other buffer is free
+                    if (lane == 0) {
+                        if (has_res || has_pre) bulk_wait_read<0>();  // the last chunk's blocks have left
+                        else bulk_wait_read<1>();                     // this block has
+                        if (has_res) {
                             advance(nu, nc);
                             if (nu < total) {
                                 fetch(nu, nc, bi ^ 1);
                                 ++fetched;
                             }
-                        } else {
-                            bulk_wait_read<1>();  // this buffer is free
                         }
                     }
                     __syncwarp();
@@ -525,10 +519,10 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                     if (has_pre) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<uint4*>(mine + 2048 + ((j ^ swz) << 4)) = narrow8<T>(&z[8 * j]);
+                            *reinterpret_cast<uint4*>(bufs + 4096 + lane * 64 + ((j ^ swz) << 4)) = narrow8<T>(&z[8 * j]);
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0 && row < d.R) tma_store_2d(&tmO.pre, bufs + 2048, col, row);
+                        if (lane == 0 && row < d.R) tma_store_2d(&tmO.pre, bufs + 4096, col, row);
                     }
                     with_act(epi.act, [&](auto act) {
 #pragma unroll
@@ -536,7 +530,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                     });
                     if (has_res) {
                         // every lane waits itself (that makes the block visible to it)
-                        const uint32_t parity = (uint32_t)(has_pre ? n : n >> 1) & 1u;
+                        const uint32_t parity = (uint32_t)(n >> 1) & 1u;
                         ok = __all_sync(0xffffffffu, mbar_wait(&res_bar[bi], parity, abort_flag));
                         if (!ok) break;
 #pragma unroll
@@ -576,7 +570,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                 if (*abort_flag) {
                     volatile int no_abort = 0;
                     for (int f = max(0, fetched - 2); f < fetched; ++f)
-                        mbar_wait(&res_bar[has_pre ? 0 : f & 1], (uint32_t)(has_pre ? f : f >> 1) & 1u, &no_abort);
+                        mbar_wait(&res_bar[f & 1], (uint32_t)(f >> 1) & 1u, &no_abort);
                     status_or(d.status, MOE_DEV_TIMEOUT);
                 }
                 bulk_wait_all();
