@@ -1134,6 +1134,7 @@ inline size_t align_up(size_t v) { return (v + 255) & ~static_cast<size_t>(255);
 // rows per CTA of the elementwise step: enough CTAs to fill the GPU a few times, at most
 // kBiasChunks along the rows, whole passes of 8 warps
 inline int act_rows(int M, int N, int vec) {
+    if (M <= 64) return 64;  // one chunk: its column sums are db already
     const int cx = ceil_div(N, 32 * vec);
     const int want = std::min(kBiasChunks, std::max(1, ceil_div(8L * num_sms(), cx)));
     return (ceil_div(M, want) + 7) / 8 * 8;
@@ -1154,12 +1155,13 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t st) {
                          (a.act == MOE_ACT_NONE || ((reinterpret_cast<uintptr_t>(a.pre) & 15) == 0 && a.ldp % 8 == 0));
         p.rows = act_rows(a.M, a.N, vec ? 8 : 1);
         const int chunks = ceil_div(a.M, p.rows);
+        if (chunks == 1 && a.db) p.part = a.db;
         const dim3 grid(ceil_div(a.N, vec ? 256 : 32), chunks);
         with_act(a.act, [&](auto act) {
             if (vec) launch_pdl(linear_act_bwd_kernel<T, 8, act.value>, grid, 256, 0, st, p);
             else launch_pdl(linear_act_bwd_kernel<T, 1, act.value>, grid, 256, 0, st, p);
         });
-        if (a.db)
+        if (a.db && chunks > 1)
             launch_pdl(linear_bias_kernel, ceil_div(a.N, 32), 256, 0, st, (const float*)p.part, chunks, a.N, a.db);
         if (cudaError_t err = cudaGetLastError()) return err;
     }

@@ -15,7 +15,7 @@
 //                           (128 x 7168: 3.0 us);
 //   norm_*_ring_kernel      many rows on the 16-byte grid: persistent CTAs behind a ring of
 //                           rows in shared memory (16384 x 7168 bf16 forward 79 us, 0.90 of
-//                           measured HBM; 8192 x 7168 backward 66 us, 0.82, of which 5 us
+//                           measured HBM; 8192 x 7168 backward 65 us, 0.83, of which 5 us
 //                           are the column sums' second kernel);
 //   norm_*_ragged_kernel    rows off the grid (8192 x 7166: forward 80 us, backward 145 us;
 //                           bound by their instructions).
@@ -284,15 +284,18 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float (*buf)[N * 32], 
 
 // R rows at a time, so that one reduction serves them all and its latency is paid once. The column sums and the weight stay in registers; x and dy are read from the
 // ring twice, before and after the rows' sums are known.
-template <typename T, int NV, int R, int S, int MAXT, bool LAYER, bool FULL>
+// GROUPED: rows that one warp holds; a CTA's warps (blockDim.y) have rows of their own.
+template <typename T, int NV, int R, int S, int MAXT, bool LAYER, bool FULL, bool GROUPED>
 __global__ void __launch_bounds__(MAXT, 1) norm_bwd_ring_kernel(NormBwd p) {
     pdl_wait();
     pdl_trigger();
     constexpr int P = kPairs<T>;
-    extern __shared__ uint4 ring[];  // [S][R rows][x, dy][nvec]
+    extern __shared__ uint4 rings[];  // per group of threads [S][R rows][x, dy][nvec]
     __shared__ float buf[2][2 * R * 32];
     int slot = 0;
     const int nvec = p.H / (2 * P), tid = threadIdx.x, nt = blockDim.x;
+    const int group = GROUPED ? threadIdx.y : 0, groups = GROUPED ? blockDim.y : 1;
+    uint4* ring = GROUPED ? rings + group * (S * R * 2 * nvec) : rings;
     const float h = (float)p.H, inv_h = 1.0f / h;
     f32x2 w[NV][P], sw[NV][P], sb[NV][P];
 #pragma unroll
@@ -318,8 +321,8 @@ __global__ void __launch_bounds__(MAXT, 1) norm_bwd_ring_kernel(NormBwd p) {
         }
         cp_async_commit();
     };
-    const long step = R * (long)gridDim.x;
-    long t = R * (long)blockIdx.x;
+    const long step = R * (long)gridDim.x * groups;
+    long t = R * ((long)blockIdx.x * groups + group);
 #pragma unroll
     for (int j = 0; j < S - 1; ++j) copy(t + j * step, ring + 2 * R * j * nvec);
     int st = 0, ahead = S - 1;
@@ -403,6 +406,13 @@ __global__ void __launch_bounds__(MAXT, 1) norm_bwd_ring_kernel(NormBwd p) {
     }
     if (!p.part) return;
     float* part = p.part + (size_t)blockIdx.x * 2 * p.H;
+    // one group writes its sums out; several add theirs, in order, in shared memory first
+    float* sums = part;
+    if constexpr (GROUPED) {
+        cp_async_wait<0>();
+        __syncthreads();
+        sums = reinterpret_cast<float*>(rings) + group * 2 * p.H;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = tid + i * nt;
@@ -410,11 +420,20 @@ __global__ void __launch_bounds__(MAXT, 1) norm_bwd_ring_kernel(NormBwd p) {
 #pragma unroll
         for (int j = 0; j < P; j += 2) {
             const float2 a = unpack2(sw[i][j]), b = unpack2(sw[i][j + 1]);
-            *reinterpret_cast<float4*>(part + (c * P + j) * 2) = make_float4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<float4*>(sums + (c * P + j) * 2) = make_float4(a.x, a.y, b.x, b.y);
             if (LAYER) {
                 const float2 d = unpack2(sb[i][j]), e = unpack2(sb[i][j + 1]);
-                *reinterpret_cast<float4*>(part + p.H + (c * P + j) * 2) = make_float4(d.x, d.y, e.x, e.y);
+                *reinterpret_cast<float4*>(sums + p.H + (c * P + j) * 2) = make_float4(d.x, d.y, e.x, e.y);
             }
+        }
+    }
+    if constexpr (GROUPED) {
+        __syncthreads();
+        const float* all = reinterpret_cast<const float*>(rings);
+        for (int c = group * nt + tid; c < (LAYER ? 2 : 1) * p.H; c += nt * groups) {
+            float v = 0.f;
+            for (int g = 0; g < groups; ++g) v += all[g * 2 * p.H + c];
+            part[c] = v;
         }
     }
 }
@@ -684,32 +703,60 @@ __global__ void __launch_bounds__(NP == 8 && S > 1 ? 512 : 1024) norm_bwd_ragged
     }
 }
 
-// dw and db from the CTAs' column sums, added in a fixed order: 32 columns per CTA,
-// 32 slices of the partial rows, then the slices.
+// dw and db from the CTAs' column sums, added in a fixed order: 32 lanes of VEC columns per
+// CTA, 32 slices of the partial rows (16 of a slice's rows loaded at once), then the slices.
+template <int VEC>
 __global__ void __launch_bounds__(1024) norm_param_kernel(const float* __restrict__ part, int n_part,
                                                           int H, float* dw, float* db) {
     pdl_wait();
     pdl_trigger();
-    __shared__ float acc[32][33];
+    __shared__ float acc[32][32 * VEC + 1];
     const int which = blockIdx.y;  // 0: dw, 1: db
     float* out = which ? db : dw;
     if (!out) return;
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    float s = 0.f;
+    const int c = (blockIdx.x * 32 + lane) * VEC;
+    float s[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s[j] = 0.f;
     if (c < H) {
         const float* src = part + (size_t)which * H + c;
-#pragma unroll 4
-        for (int i = slice; i < n_part; i += 32) s += src[(size_t)i * 2 * H];
-    }
-    acc[slice][lane] = s;
-    __syncthreads();
-    // warp `slice` sums column `slice` of the tile over the slices
-    float v = acc[lane][slice];
+        constexpr int U = 16 / VEC;
+        for (int i0 = slice; i0 < n_part; i0 += 32 * U) {
+            Pack<float, VEC> v[U];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int col = blockIdx.x * 32 + slice;
-    if (lane == 0 && col < H) out[col] = v;
+            for (int u = 0; u < U; ++u)
+                if (i0 + 32 * u < n_part)
+                    v[u] = *reinterpret_cast<const Pack<float, VEC>*>(src + (size_t)(i0 + 32 * u) * 2 * H);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i0 + 32 * u >= n_part) continue;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) s[j] += v[u].v[j];
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) acc[slice][lane * VEC + j] = s[j];
+    __syncthreads();
+    // warp `slice` sums VEC columns of the tile over the slices
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        float v = acc[lane][slice * VEC + j];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        const int col = (blockIdx.x * 32 + slice) * VEC + j;
+        if (lane == 0 && col < H) out[col] = v;
+    }
+}
+
+void launch_param(const float* part, int n_part, int H, float* dw, float* db, cudaStream_t st) {
+    if (!dw && !db) return;
+    // wide loads for few partial rows; many are spread over four times the CTAs
+    if (H % 4 == 0 && n_part <= 256)
+        launch_pdl(norm_param_kernel<4>, dim3((H + 127) / 128, db ? 2 : 1), 1024, 0, st, part, n_part, H, dw, db);
+    else
+        launch_pdl(norm_param_kernel<1>, dim3((H + 31) / 32, db ? 2 : 1), 1024, 0, st, part, n_part, H, dw, db);
 }
 
 inline int round32(int v) { return (v + 31) / 32 * 32; }
@@ -788,10 +835,6 @@ int bwd_grid(int T, int threads) {
 // no variant puts more than 16 elements of a row on a thread
 constexpr int kMaxPerThread = 16;
 
-void launch_param(const float* part, int grid, int H, float* dw, float* db, cudaStream_t st) {
-    if (part) launch_pdl(norm_param_kernel, dim3((H + 31) / 32, db ? 2 : 1), 1024, 0, st, part, grid, H, dw, db);
-}
-
 template <typename T, int NP, int R, int S>
 cudaError_t bwd_ragged(int layer, const NormBwd& p, float* dw, float* db, cudaStream_t st) {
     static_assert(2 * NP <= kMaxPerThread, "the workspace's grid bound");
@@ -806,20 +849,34 @@ cudaError_t bwd_ragged(int layer, const NormBwd& p, float* dw, float* db, cudaSt
     return cudaGetLastError();
 }
 
+template <typename T, int NV, int R, int S, int MAXT, bool LAYER>
+void (*pick_bwd_kind(bool full, bool grouped))(NormBwd) {
+    if constexpr (MAXT <= 512) {  // wider rows are never one warp's
+        if (grouped)
+            return full ? norm_bwd_ring_kernel<T, NV, R, S, 256, LAYER, true, true>
+                        : norm_bwd_ring_kernel<T, NV, R, S, 256, LAYER, false, true>;
+    }
+    return full ? norm_bwd_ring_kernel<T, NV, R, S, MAXT, LAYER, true, false>
+                : norm_bwd_ring_kernel<T, NV, R, S, MAXT, LAYER, false, false>;
+}
+template <typename T, int NV, int R, int S, int MAXT>
+void (*pick_bwd(bool layer, bool full, bool grouped))(NormBwd) {
+    return layer ? pick_bwd_kind<T, NV, R, S, MAXT, true>(full, grouped)
+                 : pick_bwd_kind<T, NV, R, S, MAXT, false>(full, grouped);
+}
+
 template <typename T, int NV, int R, int S, int MAXT>
 cudaError_t bwd_ring(int layer, const NormBwd& p, float* dw, float* db, cudaStream_t st) {
     static_assert(kFullVec<T> * NV <= kMaxPerThread, "the workspace's grid bound");
     const int threads = std::max(32, round32((p.H / kFullVec<T> + NV - 1) / NV));
-    const int smem = S * R * 2 * p.H * (int)sizeof(T);
+    const int groups = threads == 32 ? 8 : 1;
+    const int smem = groups * S * R * 2 * p.H * (int)sizeof(T);
     const bool full = p.H == threads * NV * kFullVec<T>;
-    auto kernel = layer ? (full ? norm_bwd_ring_kernel<T, NV, R, S, MAXT, true, true>
-                                : norm_bwd_ring_kernel<T, NV, R, S, MAXT, true, false>)
-                        : (full ? norm_bwd_ring_kernel<T, NV, R, S, MAXT, false, true>
-                                : norm_bwd_ring_kernel<T, NV, R, S, MAXT, false, false>);
+    auto kernel = pick_bwd<T, NV, R, S, MAXT>(layer, full, groups > 1);
     if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem)) return e;
-    const int grid = (int)std::min<long>(bwd_grid((p.T + R - 1) / R, threads),
-                                         (long)ctas_per_sm(threads, smem, 512) * num_sms());
-    if (cudaError_t e = launch_pdl(kernel, grid, threads, smem, st, p)) return e;
+    const int grid = (int)std::min<long>(bwd_grid((p.T + R * groups - 1) / (R * groups), threads),
+                                         (long)ctas_per_sm(threads * groups, smem, 512) * num_sms());
+    if (cudaError_t e = launch_pdl(kernel, grid, dim3(threads, groups), smem, st, p)) return e;
     launch_param(p.part, grid, p.H, dw, db, st);
     return cudaGetLastError();
 }
@@ -871,9 +928,7 @@ cudaError_t launch_norm_bwd(int kind, int dtype, const void* dy, long lddy, cons
                             int T, int H, const float* w, const float* mean, const float* rstd,
                             void* dx, long lddx, float* dw, float* db, float* part, cudaStream_t st) {
     if (T == 0) {  // no rows: the sums are zero
-        if (dw || db)
-            launch_pdl(norm_param_kernel, dim3((H + 31) / 32, 2), 1024, 0, st, (const float*)nullptr, 0, H,
-                       dw, db);
+        launch_param(nullptr, 0, H, dw, db, st);
         return cudaGetLastError();
     }
     const NormBwd p{dy, x, dx, w, mean, rstd, (dw || db) ? part : nullptr, lddy, ldx, lddx, T, H};
