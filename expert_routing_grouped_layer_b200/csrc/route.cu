@@ -631,7 +631,7 @@ template <typename T, int VEC, int NI>
 void fwd(const RouteParams& p, int L, cudaStream_t st) {
     // a few warps per CTA for small batches, so that they spread over the SMs
     const int warps = p.T >= 16 * num_sms() ? 8 : 2;
-    launch_pdl(route_fwd_kernel<T, VEC, NI>, (p.T + warps - 1) / warps, warps * 32, 0, st, p, L);
+    launch_pdl(route_fwd_kernel<T, VEC, NI>, (p.T - 1) / warps + 1, warps * 32, 0, st, p, L);
 }
 
 template <typename T>
@@ -682,7 +682,7 @@ cudaError_t launch_route_backward(const moe_config* c, int dtype, const void* lo
                      c->norm_topk_prob, c->score_fn, c->routed_scaling_factor};
     const int es = esize(dtype);
     const bool vec = p.E % (16 / es) == 0 && rows16(logits, ld, es) && rows16(dl, ldd, es);
-    const unsigned grid = (unsigned)((T + 7) / 8);
+    const unsigned grid = (unsigned)((T - 1) / 8 + 1);
     if (dtype == MOE_T_BF16) {
         if (vec) launch_pdl(route_bwd_kernel<__nv_bfloat16, 8>, grid, 256, 0, st, p);
         else launch_pdl(route_bwd_kernel<__nv_bfloat16, 1>, grid, 256, 0, st, p);
