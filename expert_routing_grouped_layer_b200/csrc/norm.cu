@@ -17,7 +17,7 @@
 //                           rows in shared memory (16384 x 7168 bf16 forward 79 us, 0.90 of
 //                           measured HBM; 8192 x 7168 backward 65 us, 0.83, of which 5 us
 //                           are the column sums' second kernel);
-//   norm_*_ragged_kernel    rows off the grid (8192 x 7166: forward 80 us, backward 145 us;
+//   norm_*_ragged_kernel    rows off the grid (8192 x 7166: forward 80 us, backward 150 us;
 //                           bound by their instructions).
 // The arithmetic runs two elements to an instruction (packed fp32): with single operations
 // the forward pass was bound by instruction issue (102 us).
@@ -282,9 +282,12 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float (*buf)[N * 32], 
     for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x, i);
 }
 
-// R rows at a time, so that one reduction serves them all and its latency is paid once. The column sums and the weight stay in registers; x and dy are read from the
-// ring twice, before and after the rows' sums are known.
-// GROUPED: rows that one warp holds; a CTA's warps (blockDim.y) have rows of their own.
+// R rows at a time, so that one reduction serves them all and its latency is paid once. The
+// column sums and the weight stay in registers; x and dy are read from the ring twice, before
+// and after the rows' sums are known.
+// GROUPED: rows that one warp holds. A CTA's warps (blockDim.y) have rows of their own and add
+// their column sums in shared memory, so that fewer partial rows are left for the second kernel
+// (16384 x 64 bf16: 17.4 us with a CTA per warp, 10.6 us so).
 template <typename T, int NV, int R, int S, int MAXT, bool LAYER, bool FULL, bool GROUPED>
 __global__ void __launch_bounds__(MAXT, 1) norm_bwd_ring_kernel(NormBwd p) {
     pdl_wait();
@@ -842,7 +845,7 @@ cudaError_t bwd_ragged(int layer, const NormBwd& p, float* dw, float* db, cudaSt
     const int smem = (S * 2 + 1) * R * slot_bytes(p.H * (int)sizeof(T));
     auto kernel = layer ? norm_bwd_ragged_kernel<T, NP, R, S, true> : norm_bwd_ragged_kernel<T, NP, R, S, false>;
     if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem)) return e;
-    const int grid = (int)std::min<long>(bwd_grid((p.T + R - 1) / R, threads),
+    const int grid = (int)std::min<long>(bwd_grid((p.T - 1) / R + 1, threads),
                                          (long)ctas_per_sm(threads, smem, NP == 8 ? 512 : 1024) * num_sms());
     if (cudaError_t e = launch_pdl(kernel, grid, threads, smem, st, p)) return e;
     launch_param(p.part, grid, p.H, dw, db, st);
@@ -874,7 +877,7 @@ cudaError_t bwd_ring(int layer, const NormBwd& p, float* dw, float* db, cudaStre
     const bool full = p.H == threads * NV * kFullVec<T>;
     auto kernel = pick_bwd<T, NV, R, S, MAXT>(layer, full, groups > 1);
     if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem)) return e;
-    const int grid = (int)std::min<long>(bwd_grid((p.T + R * groups - 1) / (R * groups), threads),
+    const int grid = (int)std::min<long>(bwd_grid((p.T - 1) / (R * groups) + 1, threads),
                                          (long)ctas_per_sm(threads * groups, smem, 512) * num_sms());
     if (cudaError_t e = launch_pdl(kernel, grid, dim3(threads, groups), smem, st, p)) return e;
     launch_param(p.part, grid, p.H, dw, db, st);

@@ -69,6 +69,32 @@ def test_sizes(kind, dt, T, H):
     _check(*_case(T, H, dt, T + H), 1e-6, kind)
 
 
+# Rows of one warp (up to 512 elements): whole and partial vectors of a lane, rows one by one and in
+# pairs, warps without a row, and partial sums that need many rounds of the second kernel.
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H", [(1, 512), (9, 64), (37, 512), (591, 256), (593, 504), (1500, 512), (4737, 8),
+                                 (20003, 64), (20003, 63)])
+def test_short_rows(kind, dt, T, H):
+    _check(*_case(T, H, dt, T + H), 1e-6, kind)
+
+
+@pytest.mark.parametrize("T,H", [(37, 512), (1501, 256)])
+def test_short_rows_in_place(T, H):
+    x, dy, w, b = _case(T, H, torch.bfloat16, 3)
+    mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    moe.moe_norm(x, w, b, 1e-6, torch.empty_like(x), mean, rstd)
+    ws = torch.empty(moe.moe_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device="cuda")
+    dw, db = torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+    want = torch.empty_like(x)
+    moe.moe_norm_backward(dy, x, w, mean, rstd, want, dw, db, ws)
+    for into_dy in (False, True):
+        a, g = x.clone(), dy.clone()
+        dw2, db2 = torch.empty_like(dw), torch.empty_like(db)
+        moe.moe_norm_backward(g, a, w, mean, rstd, g if into_dy else a, dw2, db2, ws)
+        assert torch.equal(g if into_dy else a, want) and torch.equal(dw, dw2) and torch.equal(db, db2)
+
+
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_many_rows(dt):
     _check(*_case(4000, 1024, dt, 1), 1e-5, "layer")
