@@ -1,8 +1,8 @@
 // binding.cpp -- tensor arguments of the row operators (norm, routing, combine gradient,
 // linear layer): reads sizes, strides, types and the current stream from torch tensors,
-// checks them and calls the C ABI of include/moe.h. The same checks written in Python cost
-// 3.8 us a call and ctypes 1.4 us, more than the kernels of a decode step run; here they
-// take 0.4 us.
+// checks them and calls the C ABI of include/moe.h. With the same checks in Python and a
+// ctypes call, a norm of 128 rows took 7.9 us of host time, more than its kernel runs; with
+// this module it takes 4.3 us, as much as the bare ctypes call with addresses at hand (4.2).
 //
 // The library's functions come by address (bind), so that one loaded libmoe.so serves both
 // this module and ctypes. Every function returns the library's status; wrong tensors raise

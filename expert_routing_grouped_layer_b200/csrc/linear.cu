@@ -16,14 +16,14 @@
 //   linear_pair_kernel   many rows: persistent CTA pairs (cta_group::2), a 256 x BN tile
 //                        per pair, accumulators double-buffered in tensor memory. Bound by
 //                        the tensor cores and the power cap: 8192 x 7168 x 2048 with bias
-//                        and residual in 168 us (1.43 PFLOP/s, tensor pipe 90% active at
+//                        and residual in 168-175 us (1.43 PFLOP/s, tensor pipe 90% active at
 //                        1.5 GHz); a library product of that size alone took 168-200;
 //   linear_split_kernel  few tiles (serving, small gradients): 128 columns x BT rows per
 //                        cluster of up to 8 CTAs that share the k range and add their
 //                        partial tiles through distributed shared memory in rank order,
 //                        so the weights stream through all SMs and equal calls give
 //                        equal bits. Bound by the weights' bytes and ~4 us of launch, set-up
-//                        and exchange: one token, 2048 x 7168, 8.2 us.
+//                        and exchange: one token, 2048 x 7168, 8.2-8.6 us.
 // Sums are fp32 in tensor memory; y, pre, dx and dW are rounded once to the tensors'
 // type, and g once between dy and the products (the tensor cores take 16-bit operands).
 #include <type_traits>
