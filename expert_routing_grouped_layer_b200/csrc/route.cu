@@ -81,14 +81,18 @@ __device__ __forceinline__ void with_score(int fn, F&& f) {
     else f(std::integral_constant<int, MOE_SCORE_SOFTMAX>());
 }
 
+// sqrt(log(1 + e^l)) = e^(l/2) (1 - e^l / 4 + ...): far below zero the first factor alone, since
+// e^l leaves the type's range while e^(l/2) is an ordinary number (from l = -88 on in fp32).
 __device__ __forceinline__ float score_f(float l, int fn, float m, float inv_z) {
     if (fn == MOE_SCORE_SIGMOID) return 1.0f / (1.0f + expf(-l));
-    if (fn == MOE_SCORE_SQRTSOFTPLUS) return sqrtf(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
+    if (fn == MOE_SCORE_SQRTSOFTPLUS)  // at -20 the other terms are 5e-10 of it
+        return l < -20.0f ? expf(0.5f * l) : sqrtf(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
     return expf(l - m) * inv_z;
 }
 __device__ __forceinline__ double score_d(double l, int fn, double m, double z) {
     if (fn == MOE_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-l));
-    if (fn == MOE_SCORE_SQRTSOFTPLUS) return sqrt(fmax(l, 0.0) + log1p(exp(-fabs(l))));
+    if (fn == MOE_SCORE_SQRTSOFTPLUS)  // at -80 they are below 2^-53
+        return l < -80.0 ? exp(0.5 * l) : sqrt(fmax(l, 0.0) + log1p(exp(-fabs(l))));
     return exp(l - m) / z;
 }
 

@@ -353,3 +353,39 @@ def test_on_another_stream_and_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(i2, idx) and torch.equal(w2, w) and torch.equal(d2, dl)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_sqrtsoftplus_far_below_zero(renorm):
+    """e^l leaves the fp32 range at -88, sqrt(log(1 + e^l)) only at -174: weights and gradients of
+    rows whose chosen logits all lie between, and around where the formula changes (-20, -80)."""
+    l = torch.full((6, 32), -300.0, device="cuda")
+    l[0, :4] = torch.tensor([-98.0, -100.3, -102.0, -103.5])
+    l[1, :4] = torch.tensor([-102.0, -103.0, -102.5, -103.4])
+    l[2, :4] = torch.tensor([-104.0, -110.0, -130.0, -150.0])
+    l[3, :4] = torch.tensor([-19.9, -20.1, -19.0, -21.0])
+    l[4, :4] = torch.tensor([-79.9, -80.1, -87.0, -89.0])
+    l[5, :4] = torch.tensor([-800.0, -801.0, -803.0, -800.5]) if renorm else torch.tensor([-30.0, -5.0, -95.0, 2.0])
+    l[5, 4:] = -1000.0
+    cfg = _cfg(32, 4, score="sqrtsoftplus", renorm=renorm)
+    idx, w = _route(cfg, l, None)
+    x = torch.where(l.double() < -40, l.double(), 0.0)
+    s = torch.where(l.double() < -40, torch.exp(x / 2), ref.scores(l.double(), "sqrtsoftplus"))
+    want, order = torch.sort(s, dim=1, descending=True, stable=True)
+    want = want[:, :4]
+    if renorm:
+        want = want / want.sum(1, keepdim=True)
+    want = 2.5 * want
+    assert torch.equal(idx.long(), order[:, :4])
+    assert ((w.double() - want).abs() <= REL * want).all()
+    # d s / d l = sig(l) / (2 s): s / 2 far below zero
+    dw = torch.tensor([[0.5, -1.0, 2.0, 0.25]], device="cuda").expand(6, 4).contiguous()
+    dl = torch.empty_like(l)
+    moe.moe_route_backward(cfg, l, idx, dw, dl)
+    at = idx.long()
+    lk, p = l.double().gather(1, at), s.gather(1, at)
+    slope = torch.where(lk < -40, 0.5, torch.sigmoid(lk) / (2 * p * p))  # over s
+    up = dw.double()
+    grad = want * slope * (up - (up * want / 2.5).sum(1, keepdim=True) if renorm else up)
+    got = dl.double().gather(1, at)
+    assert ((got - grad).abs() <= REL * want * (up.abs() + (3.75 if renorm else 0))).all()
