@@ -115,8 +115,11 @@ constexpr float kGeluCubic = 0.044715f;
 
 __device__ __forceinline__ float sigmoid_f(float z) { return rcp_approx(1.0f + exp_approx(-z)); }
 
-// tanh through one exponential: accurate to a few units of 2^-24 of 1, saturating cleanly
-__device__ __forceinline__ float tanh_f(float u) { return 1.0f - 2.0f * rcp_approx(1.0f + exp_approx(2.0f * u)); }
+// (1 + tanh u) / 2 = sigmoid(2 u) with u = sqrt(2/pi) (z + 0.044715 z^3): no difference of close
+// numbers on either side, where 1 + tanh u loses every digit below z = -4.
+__device__ __forceinline__ float gelu_tanh_arg(float z) {
+    return 2.0f * kSqrt2OverPi * fmaf(kGeluCubic * z * z, z, z);
+}
 
 // The normal distribution's Phi(z) and exp(-z^2 / 2) by Abramowitz and Stegun's 7.1.26 (erfc
 // as a polynomial in 1 / (1 + 0.3275911 x) times exp(-x^2), |error| <= 1.5e-7): no
@@ -143,8 +146,7 @@ __device__ __forceinline__ float act_f(float z) {
         float gauss;
         return z * normal_cdf(z, gauss);
     }
-    case MOE_ACT_GELU_TANH:
-        return 0.5f * z * (1.0f + tanh_f(kSqrt2OverPi * (z + kGeluCubic * z * z * z)));
+    case MOE_ACT_GELU_TANH: return z * sigmoid_f(gelu_tanh_arg(z));
     }
     return z;
 }
@@ -163,8 +165,8 @@ __device__ __forceinline__ float act_slope(float z) {
         return fmaf(z * kInvSqrt2Pi, gauss, cdf);
     }
     case MOE_ACT_GELU_TANH: {
-        const float t = tanh_f(kSqrt2OverPi * (z + kGeluCubic * z * z * z));
-        return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * kSqrt2OverPi * (1.0f + 3.0f * kGeluCubic * z * z);
+        const float v = gelu_tanh_arg(z), s = sigmoid_f(v);
+        return s + z * s * sigmoid_f(-v) * 2.0f * kSqrt2OverPi * fmaf(3.0f * kGeluCubic * z, z, 1.0f);
     }
     }
     return 1.0f;

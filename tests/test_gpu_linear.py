@@ -233,3 +233,44 @@ def test_two_streams_and_graphs():
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, out))
+
+
+def _tail(z, act):
+    """The activation in double precision without differences of close numbers."""
+    if act == "gelu_tanh":
+        return z * torch.sigmoid(2 * (2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3))
+    return ref.act(z, act)
+
+
+def _tail_case(act, dt, lo, hi, rel, n=4000):
+    """act and its slope on n values of z in [lo, hi], each off by `rel` of itself and the rounding."""
+    z = torch.linspace(lo, hi, n, dtype=torch.float64, device="cuda").to(dt)
+    want = _tail(z.double(), act)
+    one = torch.ones(1, 8, dtype=dt, device="cuda")  # rows of 16 bytes; the product has one term
+    x = torch.zeros(n, 8, dtype=dt, device="cuda")
+    x[:, 0] = z
+    for cols in (1, 128):  # a split and a pair kernel's tile
+        w = torch.zeros(cols, 8, dtype=dt, device="cuda")
+        w[:, 0] = 1
+        y = torch.empty(n, cols, dtype=dt, device="cuda")
+        moe.moe_linear(x[:, :1], w[:, :1], None, None, y, act=act)
+        off = (y.double() - want[:, None]).abs()
+        assert (off <= (ref.U[dt] + rel) * want.abs()[:, None] + TINY[dt]).all()
+    # one row of n columns: db is the slope in fp32
+    zd = z.double().requires_grad_(True)
+    slope = torch.autograd.grad(_tail(zd, act).sum(), zd)[0]
+    for cols in (n, n - 1):  # wide and element accesses
+        db = torch.empty(cols, device="cuda")
+        ws = torch.empty(moe.moe_linear_backward_workspace_bytes(1, cols, 1, act), dtype=torch.uint8, device="cuda")
+        dy = torch.ones(1, cols, dtype=dt, device="cuda")
+        w = torch.zeros(cols, 8, dtype=dt, device="cuda")
+        moe.moe_linear_backward(dy, one[:, :1], w[:, :1], z[None, :cols], None, None, db, ws, act=act)
+        assert ((db.double() - slope[:cols]).abs() <= rel * slope[:cols].abs() + 1e-38).all()
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_gelu_tanh_far_below_zero(dt):
+    """Relative to the value, which is down to 1e-26 here. The exponential's argument is at most 70
+    and off by four roundings and the instruction's 2^-23 of it, 70 * 6 * 2^-24 = 2.5e-5 relative;
+    the slope's factor of it, z (1 - s) u' ~ 30, multiplies no error of s: 2^-14 holds both."""
+    _tail_case("gelu_tanh", dt, -9.0, -3.0, 2.0 ** -14)
