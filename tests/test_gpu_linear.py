@@ -274,3 +274,25 @@ def test_gelu_tanh_far_below_zero(dt):
     and off by four roundings and the instruction's 2^-23 of it, 70 * 6 * 2^-24 = 2.5e-5 relative;
     the slope's factor of it, z (1 - s) u' ~ 30, multiplies no error of s: 2^-14 holds both."""
     _tail_case("gelu_tanh", dt, -9.0, -3.0, 2.0 ** -14)
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_gelu_far_below_zero(dt):
+    """Relative to the value, which is down to 1e-36 here. exp(-z^2 / 2) has an argument of at most 82,
+    off by two roundings and the instruction's 2^-23 of it: 82 * 4 * 2^-24 = 2.0e-5 relative; the fit
+    5e-7; the slope is -z^2 times that and more: 2^-14 holds both."""
+    _tail_case("gelu", dt, -12.8, -3.0, 2.0 ** -14)
+
+
+def test_gelu_near_zero():
+    """The slope in fp32 where it is of order one: fit 2e-7 and a dozen roundings of terms below 1.2."""
+    z = torch.linspace(-3, 3, 4096, dtype=torch.float64, device="cuda").to(HF)
+    zd = z.double().requires_grad_(True)
+    for act in ("gelu", "gelu_tanh", "silu"):
+        slope = torch.autograd.grad(_tail(zd, act).sum(), zd)[0]
+        db = torch.empty(4096, device="cuda")
+        ws = torch.empty(moe.moe_linear_backward_workspace_bytes(1, 4096, 1, act), dtype=torch.uint8, device="cuda")
+        one = torch.ones(1, 1, dtype=HF, device="cuda")
+        moe.moe_linear_backward(torch.ones(1, 4096, dtype=HF, device="cuda"), one, torch.empty(4096, 8, dtype=HF,
+                                device="cuda")[:, :1], z[None], None, None, db, ws, act=act)
+        assert ((db.double() - slope).abs() <= 2.0 ** -20).all()
