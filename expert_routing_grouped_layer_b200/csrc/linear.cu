@@ -112,7 +112,19 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kSqrt2OverPi = 0.79788456080286536f;
 constexpr float kGeluCubic = 0.044715f;
 
-__device__ __forceinline__ float sigmoid_f(float z) { return rcp_approx(1.0f + exp_approx(-z)); }
+// sigmoid(z) = f^2 r with r = 1 / (1 + e^2), e = exp(-|z| / 2), f = e below zero and 1 above. In two
+// factors it keeps its digits down to e^-174, so that z sigmoid(z) is right to where it leaves the
+// fp32 range itself (z = -92; 1 / (1 + exp(-z)) is zero from z = -87 on).
+struct Sigmoid {
+    float f, fr, other;  // other: 1 - sigmoid(z)
+    __device__ __forceinline__ explicit Sigmoid(float z) {
+        const float e = exp_approx(-0.5f * fabsf(z)), r = rcp_approx(fmaf(e, e, 1.0f));
+        f = z < 0.0f ? e : 1.0f;
+        fr = f * r;
+        other = z < 0.0f ? r : e * e * r;
+    }
+    __device__ __forceinline__ float times(float a) const { return (a * f) * fr; }
+};
 
 // (1 + tanh u) / 2 = sigmoid(2 u) with u = sqrt(2/pi) (z + 0.044715 z^3): no difference of close
 // numbers on either side, where 1 + tanh u loses every digit below z = -4.
@@ -145,12 +157,12 @@ template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
     switch (ACT) {
     case MOE_ACT_RELU: return z < 0.0f ? 0.0f : z;  // NaN stays NaN
-    case MOE_ACT_SILU: return z * sigmoid_f(z);
+    case MOE_ACT_SILU: return Sigmoid(z).times(z);
     case MOE_ACT_GELU: {
         float gauss;
         return z * normal_cdf(z, gauss);
     }
-    case MOE_ACT_GELU_TANH: return z * sigmoid_f(gelu_tanh_arg(z));
+    case MOE_ACT_GELU_TANH: return Sigmoid(gelu_tanh_arg(z)).times(z);
     }
     return z;
 }
@@ -160,8 +172,8 @@ __device__ __forceinline__ float act_slope(float z) {
     switch (ACT) {
     case MOE_ACT_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     case MOE_ACT_SILU: {
-        const float s = sigmoid_f(z);
-        return s * (1.0f + z * (1.0f - s));
+        const Sigmoid s(z);
+        return s.times(fmaf(z, s.other, 1.0f));
     }
     case MOE_ACT_GELU: {
         float gauss;
@@ -169,8 +181,8 @@ __device__ __forceinline__ float act_slope(float z) {
         return fmaf(z * kInvSqrt2Pi, gauss, cdf);
     }
     case MOE_ACT_GELU_TANH: {
-        const float v = gelu_tanh_arg(z), s = sigmoid_f(v);
-        return s + z * s * sigmoid_f(-v) * 2.0f * kSqrt2OverPi * fmaf(3.0f * kGeluCubic * z, z, 1.0f);
+        const Sigmoid s(gelu_tanh_arg(z));
+        return s.times(fmaf(z * s.other * 2.0f * kSqrt2OverPi, fmaf(3.0f * kGeluCubic * z, z, 1.0f), 1.0f));
     }
     }
     return 1.0f;

@@ -296,3 +296,10 @@ def test_gelu_near_zero():
         moe.moe_linear_backward(torch.ones(1, 4096, dtype=HF, device="cuda"), one, torch.empty(4096, 8, dtype=HF,
                                 device="cuda")[:, :1], z[None], None, None, db, ws, act=act)
         assert ((db.double() - slope).abs() <= 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("act,lo", [("silu", -95.0), ("gelu_tanh", -10.3)])
+def test_sigmoid_forms_to_the_end_of_the_range(act, lo):
+    """Down to where the value itself leaves the fp32 range (1e-38, which the tolerance allows): the
+    argument, at most 98, is off by five units of 2^-24 of it, 2.9e-5 relative."""
+    _tail_case(act, BF, lo, -3.0, 2.0 ** -14)
