@@ -167,8 +167,11 @@ __device__ __forceinline__ float act_f(float z) {
     return z;
 }
 
+// The smooth activations' slopes are 0 and 1 in fp32 long before |z| = 200; held there, an infinite
+// z (an f16 `pre` beyond 65504) or a huge one gives that instead of 0 times infinity. NaN stays NaN.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
+    if (ACT != MOE_ACT_RELU) z = z < -200.0f ? -200.0f : (z > 200.0f ? 200.0f : z);
     switch (ACT) {
     case MOE_ACT_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     case MOE_ACT_SILU: {

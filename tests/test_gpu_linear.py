@@ -303,3 +303,21 @@ def test_sigmoid_forms_to_the_end_of_the_range(act, lo):
     """Down to where the value itself leaves the fp32 range (1e-38, which the tolerance allows): the
     argument, at most 98, is off by five units of 2^-24 of it, 2.9e-5 relative."""
     _tail_case(act, BF, lo, -3.0, 2.0 ** -14)
+
+
+@pytest.mark.parametrize("act", [a for a in moe.ACT if a != "none"])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_gradient_at_infinite_and_huge_pre(act, dt):
+    """z beyond the f16 range is kept as an infinite pre; its slope is still 0 or 1."""
+    big = [1e20, 3e38] if dt == BF else [5e4, 65504.0]
+    pre = torch.tensor([[float("inf"), *big, 300.0, -float("inf"), *(-b for b in big), -300.0, float("nan")]],
+                       device="cuda").to(dt)
+    N = pre.shape[1]
+    db, g = torch.empty(N, device="cuda"), torch.empty(N, 1, dtype=dt, device="cuda")
+    ws = torch.empty(moe.moe_linear_backward_workspace_bytes(1, N, 1, act), dtype=torch.uint8, device="cuda")
+    dy = torch.full((1, N), 2.0, dtype=dt, device="cuda")
+    one, w = torch.ones(1, 1, dtype=dt, device="cuda"), torch.ones(N, 8, dtype=dt, device="cuda")[:, :1]
+    moe.moe_linear_backward(dy, one, w, pre, None, g, db, ws, act=act)
+    want = torch.tensor([2.0] * 4 + [0.0] * 4, device="cuda")
+    assert torch.equal(db[:8], want) and torch.isnan(db[8])
+    assert torch.equal(g[:8, 0].float(), want) and torch.isnan(g[8, 0])
