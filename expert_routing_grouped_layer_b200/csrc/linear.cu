@@ -115,16 +115,10 @@ constexpr float kGeluCubic = 0.044715f;
 // sigmoid(z) = f^2 r with r = 1 / (1 + e^2), e = exp(-|z| / 2), f = e below zero and 1 above. In two
 // factors it keeps its digits down to e^-174, so that z sigmoid(z) is right to where it leaves the
 // fp32 range itself (z = -92; 1 / (1 + exp(-z)) is zero from z = -87 on).
-struct Sigmoid {
-    float f, fr, other;  // other: 1 - sigmoid(z)
-    __device__ __forceinline__ explicit Sigmoid(float z) {
-        const float e = exp_approx(-0.5f * fabsf(z)), r = rcp_approx(fmaf(e, e, 1.0f));
-        f = z < 0.0f ? e : 1.0f;
-        fr = f * r;
-        other = z < 0.0f ? r : e * e * r;
-    }
-    __device__ __forceinline__ float times(float a) const { return (a * f) * fr; }
-};
+__device__ __forceinline__ float times_sigmoid(float a, float z) {
+    const float e = exp_approx(-0.5f * fabsf(z)), r = rcp_approx(fmaf(e, e, 1.0f)), f = z < 0.0f ? e : 1.0f;
+    return (a * f) * (f * r);
+}
 
 // (1 + tanh u) / 2 = sigmoid(2 u) with u = sqrt(2/pi) (z + 0.044715 z^3): no difference of close
 // numbers on either side, where 1 + tanh u loses every digit below z = -4.
@@ -132,15 +126,14 @@ __device__ __forceinline__ float gelu_tanh_arg(float z) {
     return 2.0f * kSqrt2OverPi * fmaf(kGeluCubic * z * z, z, z);
 }
 
-// The normal distribution's Phi(z) and exp(-z^2 / 2): Phi(-x) = exp(-x^2 / 2) R(x), where R goes
-// from 1/2 to 1 / (x sqrt(2 pi)) and is fitted as a polynomial in t = 1 / (1 + 0.3 x) that keeps the
-// largest relative error over 0 <= x <= 14.5 least (1.7e-7; a linear program over R = erfcx(x /
-// sqrt 2) / 2): the tail is right relative to itself, and there is no branch and no more than two
+// The normal distribution's Phi(-x) = exp(-x^2 / 2) R(x) for x >= 0, where R goes from 1/2 to
+// 1 / (x sqrt(2 pi)) and is fitted as a polynomial in t = 1 / (1 + 0.3 x) that keeps the largest
+// relative error over 0 <= x <= 14.5 least (1.7e-7; a linear program over R = erfcx(x / sqrt 2) / 2):
+// the tail is right relative to itself, and there is no branch and no more than two
 // special-function operations. erff's two ranges diverge within a warp; with it the GELU epilogue
 // took 11.6 us a tile.
-__device__ __forceinline__ float normal_cdf(float z, float& gauss) {
-    const float x = fabsf(z);
-    gauss = exp_approx(-0.5f * x * x);
+__device__ __forceinline__ float normal_gauss(float x) { return exp_approx(-0.5f * x * x); }
+__device__ __forceinline__ float normal_ratio(float x) {
     const float t = rcp_approx(fmaf(0.3f, x, 1.0f));
     float p = fmaf(t, 0.035431112f, -0.156189101f);
     p = fmaf(t, p, 0.204609411f);
@@ -149,46 +142,49 @@ __device__ __forceinline__ float normal_cdf(float z, float& gauss) {
     p = fmaf(t, p, 0.100168327f);
     p = fmaf(t, p, 0.120713345f);
     p = fmaf(t, p, 0.119631929f);
-    const float tail = p * t * gauss;  // Phi(-|z|)
-    return z < 0.0f ? tail : 1.0f - tail;
+    return p * t;
 }
 
 template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
     switch (ACT) {
     case MOE_ACT_RELU: return z < 0.0f ? 0.0f : z;  // NaN stays NaN
-    case MOE_ACT_SILU: return Sigmoid(z).times(z);
+    case MOE_ACT_SILU: return times_sigmoid(z, z);
     case MOE_ACT_GELU: {
-        float gauss;
-        return z * normal_cdf(z, gauss);
+        const float x = fabsf(z), tail = normal_ratio(x) * normal_gauss(x);
+        return z * (z < 0.0f ? tail : 1.0f - tail);
     }
-    case MOE_ACT_GELU_TANH: return Sigmoid(gelu_tanh_arg(z)).times(z);
+    case MOE_ACT_GELU_TANH: return times_sigmoid(z, gelu_tanh_arg(z));
     }
     return z;
 }
 
-// The smooth activations' slopes are 0 and 1 in fp32 long before |z| = 200; held there, an infinite
-// z (an f16 `pre` beyond 65504) or a huge one gives that instead of 0 times infinity. NaN stays NaN.
+// The smaller number, NaN if one is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Each smooth activation is a(z) = z S(z) with S(z) + S(-z) = 1, so a'(z) = 1 - a'(-z): the slope is
+// worked out below zero, where it is right relative to itself. Long before |z| = 200 it is 0 and 1 in
+// fp32; held there, an infinite z (an f16 `pre` beyond 65504) or a huge one gives that instead of 0
+// times infinity.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
-    if (ACT != MOE_ACT_RELU) z = z < -200.0f ? -200.0f : (z > 200.0f ? 200.0f : z);
-    switch (ACT) {
-    case MOE_ACT_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-    case MOE_ACT_SILU: {
-        const Sigmoid s(z);
-        return s.times(fmaf(z, s.other, 1.0f));
+    if (ACT == MOE_ACT_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    if (ACT == MOE_ACT_NONE) return 1.0f;
+    const float x = min_nan(fabsf(z), 200.0f);
+    float below;  // a'(-x)
+    if (ACT == MOE_ACT_GELU) {
+        below = normal_gauss(x) * fmaf(x, -kInvSqrt2Pi, normal_ratio(x));
+    } else {  // a'(-x) = sigmoid(-v) (1 - x sigmoid(v) v'(x)), the exponential in two factors as above
+        const float v = ACT == MOE_ACT_SILU ? x : gelu_tanh_arg(x);
+        const float e = exp_approx(-0.5f * v), r = rcp_approx(fmaf(e, e, 1.0f));
+        const float xv = ACT == MOE_ACT_SILU ? x : x * fmaf(6.0f * kSqrt2OverPi * kGeluCubic * x, x, 2.0f * kSqrt2OverPi);
+        below = (e * fmaf(-xv, r, 1.0f)) * (e * r);
     }
-    case MOE_ACT_GELU: {
-        float gauss;
-        const float cdf = normal_cdf(z, gauss);
-        return fmaf(z * kInvSqrt2Pi, gauss, cdf);
-    }
-    case MOE_ACT_GELU_TANH: {
-        const Sigmoid s(gelu_tanh_arg(z));
-        return s.times(fmaf(z * s.other * 2.0f * kSqrt2OverPi, fmaf(3.0f * kGeluCubic * z, z, 1.0f), 1.0f));
-    }
-    }
-    return 1.0f;
+    return z < 0.0f ? below : 1.0f - below;
 }
 
 // Calls f with the activation as a compile-time constant: one branch for a group of values.
