@@ -349,7 +349,8 @@ moe_status moe_layer_forward_prenorm(const moe_config *cfg, const void *x, int32
  *  (ones, zeros). mean, rstd: fp32 [T], written for the backward pass, each may be
  *  NULL; mean is not written for MOE_NORM_RMS. eps finite, >= 0. 1 <= H <= 16384,
  *  larger rows return MOE_ERR_UNSUPPORTED. Statistics and arithmetic are fp32, y is
- *  rounded once. Rows whose base, stride and length are multiples of 16 bytes move
+ *  rounded once; a row of finite values whose (centred) squares add up to more than
+ *  fp32 holds has rstd = 0 and so y = b. Rows whose base, stride and length are multiples of 16 bytes move
  *  by 16-byte accesses; others element by element. */
 moe_status moe_norm(int32_t kind, int32_t dtype, const void *x, int64_t ldx, int32_t T, int32_t H,
                     const float *w, const float *b, float eps, void *y, int64_t ldy, float *mean,

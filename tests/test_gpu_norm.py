@@ -252,3 +252,28 @@ def test_two_captured_graphs_on_another_stream():
             step()
             s.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(got, out))
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [1024, 1023])
+def test_large_rows_have_one_outcome(H, dt, kind):
+    """Rows whose squares add up to more than fp32 holds get rstd 0 and y = b, those just below it are
+    right, whichever kernel the batch size and the alignment choose."""
+    g = torch.Generator(device="cuda").manual_seed(H)
+    w, b = 1 + 0.3 * torch.randn(H, generator=g, device="cuda"), 0.2 * torch.randn(H, generator=g, device="cuda")
+    rows = torch.randn(3, H, generator=g, device="cuda")
+    rows = (rows / rows.abs().max() * torch.tensor([[1e20], [4e17], [1e18]], device="cuda")).to(dt)
+    for T in (3, 64, 700):
+        x = torch.randn(T, H, generator=g, device="cuda").to(dt)
+        x[:3] = rows
+        y, mean, rstd = torch.empty_like(x), torch.zeros(T, device="cuda"), torch.empty(T, device="cuda")
+        moe.moe_norm(x, w, b, 1e-6, y, mean if kind == "layer" else None, rstd, kind=kind)
+        assert rstd[0] == 0 and torch.equal(y[0], b.to(dt)) and torch.isfinite(y).all()
+        _, m, r = ref.norm(x[1:3], w, b, 1e-6, kind)
+        assert ((rstd[1:3].double() - r).abs() <= E32 * r * (1 + (m * r) ** 2)).all()
+        dx, dw, db = torch.empty_like(x), torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+        ws = torch.empty(moe.moe_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device="cuda")
+        moe.moe_norm_backward(torch.ones_like(x), x, w, mean if kind == "layer" else None, rstd, dx, dw, db, ws,
+                              kind=kind)
+        assert (dx[0] == 0).all() and torch.isfinite(dx).all() and torch.isfinite(dw).all()
