@@ -26,6 +26,7 @@
 #include <cmath>
 
 #include "internal.h"
+#include "row_chunks.h"
 #include "sm100.cuh"
 #include "types.cuh"
 
@@ -463,21 +464,32 @@ __host__ __device__ constexpr int slot_bytes(int row_bytes) { return (row_bytes 
 template <typename T>
 __device__ __forceinline__ int row_offset(const T* p) { return (int)(reinterpret_cast<uintptr_t>(p) & 15); }
 
-// Copies row t of a matrix (T rows of H elements) into `slot` at the row's own offset. The
-// chunks at a row's ends bring neighbouring bytes along, which nothing reads; where they
-// would lie outside the matrix (the first and last row) single elements are copied.
+// A matrix whose rows are copied below.
 template <typename T>
-__device__ __forceinline__ void copy_row_in(uint8_t* slot, const T* m, long ld, long t, int n_rows, int H) {
-    const uint8_t* p = reinterpret_cast<const uint8_t*>(m + t * ld);
-    const int off = row_offset(m + t * ld), end = off + H * (int)sizeof(T);
-    const uint8_t* base = p - off;
-    const bool first = t == 0, last = t == n_rows - 1;
-    for (int c = threadIdx.x * 16; c < end; c += blockDim.x * 16) {
-        if ((first && c < off) || (last && c + 16 > end)) {
-            for (int i = max(c, off); i < min(c + 16, end); i += (int)sizeof(T))
-                *reinterpret_cast<T*>(slot + i) = *reinterpret_cast<const T*>(base + i);
-        } else {
+struct Rows {
+    const T* m;
+    long ld;
+    uintptr_t last;  // one past its last byte
+    int H;
+    __device__ __forceinline__ Rows(const void* p, long ld, int n_rows, int H)
+        : m(static_cast<const T*>(p)), ld(ld), last(reinterpret_cast<uintptr_t>(m + (n_rows - 1) * ld + H)), H(H) {}
+    __device__ __forceinline__ const T* row(long t) const { return m + t * ld; }
+};
+
+// Copies row t into `slot` at the row's own offset. The chunks at a row's ends bring neighbouring
+// bytes along, which nothing reads; chunks that would reach outside the matrix are copied element
+// by element.
+template <typename T>
+__device__ __forceinline__ void copy_row_in(uint8_t* slot, const Rows<T>& a, long t) {
+    const T* p = a.row(t);
+    const RowChunks r(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(a.m), a.last, a.H * (int)sizeof(T));
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(p) - r.off;
+    for (int c = threadIdx.x * 16; c < r.end; c += blockDim.x * 16) {
+        if (r.whole(c)) {
             cp_async16(slot + c, base + c);
+        } else {
+            for (int i = max(c, r.off); i < min(c + 16, r.end); i += (int)sizeof(T))
+                *reinterpret_cast<T*>(slot + i) = *reinterpret_cast<const T*>(base + i);
         }
     }
 }
@@ -552,12 +564,12 @@ __global__ void __launch_bounds__(1024) norm_fwd_ragged_kernel(NormFwd p) {
     const Own<NP> own(H);
     read_param<NP>(w, p.w, own, 1.f);
     read_param<NP>(b, p.b, own, 0.f);
-    const T* x = static_cast<const T*>(p.x);
+    const Rows<T> x(p.x, p.ldx, p.T, H);
     const long step = gridDim.x;
     long t = blockIdx.x;
 #pragma unroll
     for (int j = 0; j < S - 1; ++j) {
-        if (t + j * step < p.T) copy_row_in<T>(slots + j * SL, x, p.ldx, t + j * step, p.T, H);
+        if (t + j * step < p.T) copy_row_in<T>(slots + j * SL, x, t + j * step);
         cp_async_commit();
     }
     int st = 0;
@@ -565,11 +577,11 @@ __global__ void __launch_bounds__(1024) norm_fwd_ragged_kernel(NormFwd p) {
         cp_async_wait<S - 2>();
         __syncthreads();  // the row is in; every thread has left the slot before it
         const long ahead = t + (S - 1) * step;
-        if (ahead < p.T) copy_row_in<T>(slots + (st == 0 ? S - 1 : st - 1) * SL, x, p.ldx, ahead, p.T, H);
+        if (ahead < p.T) copy_row_in<T>(slots + (st == 0 ? S - 1 : st - 1) * SL, x, ahead);
         cp_async_commit();
         uint8_t* slot = slots + st * SL;
         f32x2 v[NP];
-        read_row<T, NP>(v, slot + row_offset(x + t * p.ldx), own);
+        read_row<T, NP>(v, slot + row_offset(x.row(t)), own);
         float mean = 0.f;
         if (LAYER) {
             f32x2 sum = v[0];
@@ -615,14 +627,13 @@ __global__ void __launch_bounds__(NP == 8 && S > 1 ? 512 : 1024) norm_bwd_ragged
     read_param<NP>(w, p.w, own, 1.f);
 #pragma unroll
     for (int i = 0; i < NP; ++i) sw[i] = sb[i] = pack2(0.f, 0.f);
-    const T* x = static_cast<const T*>(p.x);
-    const T* dy = static_cast<const T*>(p.dy);
+    const Rows<T> x(p.x, p.ldx, p.T, H), dy(p.dy, p.lddy, p.T, H);
     auto copy = [&](long t, uint8_t* to) {
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             if (t + q < p.T) {
-                copy_row_in<T>(to + 2 * q * SL, x, p.ldx, t + q, p.T, H);
-                copy_row_in<T>(to + (2 * q + 1) * SL, dy, p.lddy, t + q, p.T, H);
+                copy_row_in<T>(to + 2 * q * SL, x, t + q);
+                copy_row_in<T>(to + (2 * q + 1) * SL, dy, t + q);
             }
         }
         cp_async_commit();
@@ -653,8 +664,8 @@ __global__ void __launch_bounds__(NP == 8 && S > 1 ? 512 : 1024) norm_bwd_ragged
         float s[2 * R];
         // n and the weighted dy of row q; where the row ends they are zero
         auto row = [&](int q, f32x2 (&n)[NP], f32x2 (&g)[NP]) {
-            read_row<T, NP>(n, rows + 2 * q * SL + row_offset(x + (t + q) * p.ldx), own);
-            read_row<T, NP>(g, rows + (2 * q + 1) * SL + row_offset(dy + (t + q) * p.lddy), own);
+            read_row<T, NP>(n, rows + 2 * q * SL + row_offset(x.row(t + q)), own);
+            read_row<T, NP>(g, rows + (2 * q + 1) * SL + row_offset(dy.row(t + q)), own);
             const f32x2 minus = pack2(-mean[q], -mean[q]), r2 = pack2(r[q], r[q]);
 #pragma unroll
             for (int i = 0; i < NP; ++i) n[i] = mul2(LAYER ? add2(n[i], minus) : n[i], r2);

@@ -277,3 +277,16 @@ def test_large_rows_have_one_outcome(H, dt, kind):
         moe.moe_norm_backward(torch.ones_like(x), x, w, mean if kind == "layer" else None, rstd, dx, dw, db, ws,
                               kind=kind)
         assert (dx[0] == 0).all() and torch.isfinite(dx).all() and torch.isfinite(dw).all()
+
+
+@pytest.mark.parametrize("H,ld", [(1, 1), (1, 2), (2, 2), (3, 3), (3, 5), (5, 7), (7, 7), (7, 9)])
+def test_rows_of_few_bytes_between_other_data(H, ld):
+    """NaN in front of, between and behind rows of fewer than 16 bytes reaches nothing."""
+    for T in (1, 2, 3, 9, 700):
+        for off in (0, 1, 3, 7):
+            flat = torch.full((T * ld + 64,), float("nan"), dtype=torch.bfloat16, device="cuda")
+            x = flat[off:off + T * ld].view(T, ld)[:, :H]
+            x.copy_(torch.randn(T, H, generator=torch.Generator(device="cuda").manual_seed(T), device="cuda"))
+            before = flat.clone()
+            _check(x, x.clone(), None, None, 1e-6, "rms")
+            assert torch.equal(flat.view(torch.int16), before.view(torch.int16))
