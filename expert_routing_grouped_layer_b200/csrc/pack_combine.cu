@@ -275,8 +275,11 @@ __global__ void __launch_bounds__(128) combine_token_kernel(const __nv_bfloat16*
         for (int i = 0; i < 8; ++i) acc[i] = 0.f;
         for (int j = 0; j < k; ++j) {
             const int r = rows[j];
-            if (r < 0) continue;
             const float wj = wts[j];
+            if (r < 0) {  // no row: adds nothing, unless the weight is NaN
+                if (wj != wj) acc[0] = acc[1] = acc[2] = acc[3] = acc[4] = acc[5] = acc[6] = acc[7] = wj;
+                continue;
+            }
             const uint4 u = *reinterpret_cast<const uint4*>(y + (size_t)r * H + (size_t)v * 8);
             const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&u);
 #pragma unroll
@@ -351,8 +354,11 @@ __global__ void __launch_bounds__(128) combine_kernel(const __nv_bfloat16* __res
 #pragma unroll
     for (int j = 0; j < MAXR; ++j) {
         if (j < k) {
-            if (rows[j] < 0) continue;
             const float wj = wts[j];
+            if (rows[j] < 0) {
+                if (wj != wj) acc[0] = acc[1] = acc[2] = acc[3] = acc[4] = acc[5] = acc[6] = acc[7] = wj;
+                continue;
+            }
             const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&u[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

@@ -290,7 +290,9 @@ moe_status moe_grouped_swiglu(const moe_config *cfg, const void *x, int32_t T,
 /* Weighted scatter-back combine ([V3] 三.4 "按原顺序放回，乘上 top-k 权重求和" and
  * the shared-expert addition in DeepseekV3MoE.forward):
  *   out[t] = bf16( sum_j topk_w[t][j] * y[row_of[t*k+j]] + sum_s shared_y[s][t] ),
- * summed in fp32 in slot order then shared order, rounded once.
+ * summed in fp32 in slot order then shared order, rounded once. A pair without a row
+ * (row_of < 0) adds nothing; where its weight is NaN (moe_route's sign of a row with a
+ * NaN or +inf logit) the token's output is NaN.
  *  y bf16 [N][H]; shared_y bf16 [S][T][H] (may be NULL when S = 0);
  *  row_of int32 [N]; topk_w fp32 [T][k]; out bf16 [T][H]. */
 moe_status moe_combine(const moe_config *cfg, const void *y, const void *shared_y,

@@ -152,3 +152,28 @@ def test_two_blocks_at_once():
     torch.cuda.synchronize()
     for b, w in zip(blocks, want):
         assert all(torch.equal(a, r) for a, r in zip(w, b.results()))
+
+
+@pytest.mark.parametrize("T", [6, 3000])
+def test_nan_weight_of_a_pair_without_a_row_reaches_the_output(T):
+    """On both sides of the combine's small-batch path; finite weights of such pairs add nothing."""
+    cfg = W.CONFIGS["tiny_bf16"]
+    H, k = cfg.hidden, cfg.num_experts_per_tok
+    S = cfg.n_shared_experts
+    g = torch.Generator(device="cuda").manual_seed(T)
+    y, sy = torch.randn(T * k, H, generator=g, device="cuda").to(BF), torch.randn(S, T, H, generator=g, device="cuda").to(BF)
+    row_of = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32)
+    w = torch.rand(T, k, generator=g, device="cuda")
+    row_of.view(T, k)[1:4] = -1
+    row_of.view(T, k)[4, 1:] = -1
+    out, want = torch.empty(T, H, dtype=BF, device="cuda"), torch.empty(T, H, dtype=BF, device="cuda")
+    moe.moe_combine(cfg, y, sy, row_of, w, T, want)
+    w[2], w[4, 1] = float("nan"), float("nan")
+    moe.moe_combine(cfg, y, sy, row_of, w, T, out)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[[2, 4]] = False
+    assert torch.isnan(out[[2, 4]]).all()
+    assert torch.equal(out[keep], want[keep]) and torch.isfinite(want).all()
+    w[2], w[4, 1] = 3.0, 5.0
+    moe.moe_combine(cfg, y, sy, row_of, w, T, out)
+    assert torch.equal(out, want)
