@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(256) perm_count_kernel(const int32_t* __restri
         if (p >= N) break;
         const int e = idx[p];
         if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
-        else bad = true;
+        else bad |= e != -1;  // -1: no expert
     }
     if (bad) status_or(status, MOE_DEV_BAD_EXPERT);
     __syncthreads();
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(PERM_WARPS * 32) perm_single_kernel(
         const long p = wstart + 32 * i + lane;
         const int e = ev[i];
         const bool ok = p < N && e >= 0 && e < E;
-        bad |= p < N && !ok;
+        bad |= p < N && !ok && e != -1;  // -1: no expert
         const unsigned act = __ballot_sync(0xffffffffu, ok);
         if (ok) {
             const unsigned m = __match_any_sync(act, e);

@@ -65,7 +65,7 @@ typedef enum {
 } moe_status;
 
 /* bits OR-ed into *dev_status by kernels */
-#define MOE_DEV_BAD_EXPERT 1 /* a topk_idx entry outside [0, E): pair skipped    */
+#define MOE_DEV_BAD_EXPERT 1 /* a topk_idx entry below -1 or >= E: pair skipped  */
 #define MOE_DEV_TIMEOUT 2    /* a pipeline wait exceeded its limit: work dropped */
 
 /* scoring function ([V3] 三.1 sigmoid; [V4] 架构 sqrtsoftplus = sqrt(softplus)) */
@@ -195,10 +195,11 @@ moe_status moe_gate_topk(const moe_config *cfg, const void *x, int32_t T, const 
 /* Dispatch permutation ([V3] 三.4: count tokens per expert, argsort by expert id).
  *  topk_idx int32 [T][k]. Pairs p = t*k + j are ordered by (expert, p)
  *  ascending, a stable sort that is deterministic run to run.
- *  expert_offsets int32 [E+1]: start row of each expert's block, [E] = N;
- *  sorted_pair int32 [N]: the pair index at each row; row_of int32 [N]: the
- *  row of each pair (the inverse). Pairs with an expert id outside [0, E) are
- *  left out (row_of = -1) and MOE_DEV_BAD_EXPERT is set in *dev_status. */
+ *  expert_offsets int32 [E+1]: start row of each expert's block, [E] = N less the
+ *  pairs left out; sorted_pair int32 [N]: the pair index at each row below [E] (not
+ *  written from there on); row_of int32 [N]: the row of each pair (the inverse).
+ *  Pairs with an expert id outside [0, E) are left out (row_of = -1). Id -1 is "no
+ *  expert" (moe_route's empty slots); any other sets MOE_DEV_BAD_EXPERT in *dev_status. */
 moe_status moe_permute(const moe_config *cfg, const int32_t *topk_idx, int32_t T,
                        int32_t *expert_offsets, int32_t *sorted_pair, int32_t *row_of,
                        int32_t *dev_status, void *ws, size_t ws_bytes, void *stream);
@@ -382,7 +383,7 @@ size_t moe_norm_backward_workspace_bytes(int32_t T, int32_t H);
  *  - An expert whose logit or bias is -inf is masked: it is never chosen (a -inf logit
  *    also has s = 0). A group's score is the sum of its two largest unmasked s' (its one
  *    unmasked s'; a group without any is kept last). Where fewer than k experts can be
- *    chosen, the remaining slots hold -1 with weight 0, and moe_permute leaves them out.
+ *    chosen, the remaining slots hold -1 ("no expert" to moe_permute) with weight 0.
  *  - A row with a NaN or +inf logit (or any such bias) gets -1 in every slot and NaN
  *    weights.
  *  - The order of s' is decided exactly: as in double precision, then by the larger

@@ -177,3 +177,72 @@ def test_nan_weight_of_a_pair_without_a_row_reaches_the_output(T):
     w[2], w[4, 1] = 3.0, 5.0
     moe.moe_combine(cfg, y, sy, row_of, w, T, out)
     assert torch.equal(out, want)
+
+
+def _permute(cfg, idx, T):
+    N, E = T * cfg.num_experts_per_tok, cfg.n_routed_experts
+    e = lambda n: torch.full((n,), -7, dtype=torch.int32, device="cuda")
+    off, pairs, row_of, st = e(E + 1), e(N), e(N), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(moe.moe_workspace_bytes(cfg, T), dtype=torch.uint8, device="cuda")
+    moe.moe_permute(cfg, idx, T, off, pairs, row_of, st, ws)
+    return off, pairs, row_of, st.item()
+
+
+@pytest.mark.parametrize("T", [9, 3000])  # one CTA, and several chunks of pairs
+def test_permute_takes_minus_one_as_no_expert(T):
+    cfg = W.CONFIGS["tiny_bf16"]
+    k, E = cfg.num_experts_per_tok, cfg.n_routed_experts
+    idx = torch.randint(0, E, (T, k), dtype=torch.int32, device="cuda", generator=torch.Generator(device="cuda").manual_seed(T))
+    idx[2], idx[5, 1:], idx[T - 1] = -1, -1, -1
+    off, pairs, row_of, st = _permute(cfg, idx, T)
+    flat = idx.view(-1)
+    has = flat >= 0
+    n = int(has.sum())
+    order = torch.sort(torch.where(has, flat, E), stable=True)[1][:n]
+    assert st == 0 and off[E].item() == n
+    assert torch.equal(pairs[:n].long(), order) and (pairs[n:] == -7).all()
+    assert (row_of[~has] == -1).all() and torch.equal(row_of[order].long(), torch.arange(n, device="cuda"))
+    for bad in (-2, E):  # any other id outside the range is an error
+        idx[3, 0] = bad
+        assert _permute(cfg, idx, T)[3] == moe.MOE_DEV_BAD_EXPERT
+
+
+@pytest.mark.parametrize("T", [50, 2500])
+def test_padded_and_nan_tokens(T):
+    """Masked (padded) tokens, tokens with fewer experts than k and a token with a NaN logit through the
+    routing, the permutation, the experts, the combine and back. Tolerance: the combine's one rounding
+    (2^-8 of the result) and fp32 sums of at most 16 terms."""
+    b = Block(T, T + 1)
+    c, k, E = b.cfg, b.cfg.num_experts_per_tok, b.cfg.n_routed_experts
+    pad = torch.arange(T, device="cuda") % 7 == 3
+    moe.moe_norm(b.x, b.nw, b.nb, 1e-6, b.h, b.mean, b.rstd)
+    moe.moe_linear(b.h, b.wr, None, None, b.logits, dev_status=b.status)
+    b.logits[pad] = -float("inf")
+    b.logits[1, 2:] = -float("inf")
+    b.logits[2, 5] = float("nan")
+    moe.moe_route(c, b.logits, b.bias, b.idx, b.w)
+    moe.moe_permute(c, b.idx, T, b.off, b.pairs, b.row_of, b.status, b.ws)
+    assert (b.idx[pad] == -1).all() and (b.idx[2] == -1).all() and (b.idx[1] >= 0).sum() == 2
+    b.y.fill_(float("nan"))  # rows that no pair has stay so, and reach nothing
+    moe.moe_grouped_swiglu(c, b.h, T, b.pairs, b.off, b.experts, b.y, b.sy, b.ws, b.status)
+    moe.moe_combine(c, b.y, b.sy, b.row_of, b.w, T, b.out)
+    assert b.status.item() == 0
+    has = b.row_of.view(T, k) >= 0
+    assert torch.equal(has, b.idx >= 0) and b.off[E].item() == has.sum().item()
+    rows = b.y.double()[b.row_of.long().clamp(min=0)].view(T, k, -1)
+    terms = torch.where(has[:, :, None], b.w.double()[:, :, None] * rows, 0.0)
+    want = terms.sum(1) + b.sy.double().sum(0)
+    size = terms.abs().sum(1) + b.sy.double().abs().sum(0)
+    good = torch.ones(T, dtype=torch.bool, device="cuda")
+    good[2] = False
+    assert torch.isnan(b.out[2]).all()
+    assert ((b.out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * size)[good].all()
+    # and back: empty slots get no gradient, padded rows none at all
+    moe.moe_combine_backward(c, b.dout, b.y, b.row_of, b.w, b.dy, b.dw)
+    assert torch.isfinite(b.dy).all() and (b.dw[~has] == 0).all() and torch.isfinite(b.dw).all()
+    b.dw[~has] = float("nan")
+    moe.moe_route_backward(c, b.logits, b.idx, b.dw, b.dlogits)
+    assert torch.isfinite(b.dlogits).all() and (b.dlogits[pad] == 0).all() and (b.dlogits[2] == 0).all()
+    moe.moe_linear_backward(b.dlogits, b.h, b.wr, None, b.dh, b.dwr, None, b.ops_ws, dev_status=b.status)
+    moe.moe_norm_backward(b.dh, b.x, b.nw, b.mean, b.rstd, b.dx, b.dnw, b.dnb, b.ops_ws)
+    assert (b.dx[pad] == 0).all() and torch.isfinite(b.dnw).all() and b.status.item() == 0
