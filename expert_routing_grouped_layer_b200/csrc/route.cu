@@ -338,7 +338,8 @@ __global__ void __launch_bounds__(256, NI * VEC > 32 ? 1 : 3) route_fwd_kernel(R
             b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
             b1 = fmaxf(b1, o1);
         }
-        const float gs = b2 == -kInf ? b1 : b1 + b2;
+        // half the sum: two biases of the type's lowest value add up to a number, above "no expert"
+        const float gs = 0.5f * b1 + (b2 == -kInf ? 0.f : 0.5f * b2);
         const bool real = g < p.n_group;
         keep = false;
         uint32_t gk = real ? key_of(gs) : 0u, lo_key = 0u;
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(256, NI * VEC > 32 ? 1 : 3) route_fwd_kernel(R
         const float lo = value_of(lo_key);                       // smallest kept
         const float hi = hi_key ? value_of(hi_key) : -kInf;      // largest left out
         const float mag = warp_max(real && b1 != -kInf ? fmaxf(fabsf(b1), b2 == -kInf ? 0.f : fabsf(b2)) : 0.f);
-        const float tol = 5.f * bound(mag);  // two sums of two values each
+        const float tol = 2.5f * bound(mag);  // two halved sums of two values each
         if (hi != -kInf && !(lo - hi > tol)) {
             const double zd = p.score_fn == MOE_SCORE_SOFTMAX ? row_z<T>(row, p.E, m) : 1.0;
             const uint32_t kept = groups_exact<T>(Row<T>{row, p.bias, p.E, gsz, p.score_fn, m, zd, kFull},
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(256, NI * VEC > 32 ? 1 : 3) route_fwd_kernel(R
     float least = -FLT_MAX;
     if (tau != 0u) {
         least = value_of(tau);
-        if (!by_logit) least -= 2.f * bound(least);
+        if (!by_logit) least = fmaxf(least - 2.f * bound(least), -FLT_MAX);  // never the masked
     }
     // the elements not below `from`, as bits and (up to 32 of them) in the warp's list
     Bits avail;
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(256, NI * VEC > 32 ? 1 : 3) route_fwd_kernel(R
         bool near = lane + 1 < p.k && next_key != 0u && my_v - value_of(next_key) <= 2.f * bound(my_v) &&
                     !(next_l == my_l && next_b == my_b);
         const int chosen = min(p.k, total);
-        const float last_v = value_of(last), cut = last_v - 2.f * bound(last_v);
+        const float last_v = value_of(last), cut = fmaxf(last_v - 2.f * bound(last_v), -FLT_MAX);
         const float ll = __shfl_sync(kFull, my_l, chosen - 1), lb = __shfl_sync(kFull, my_b, chosen - 1);
         auto as_last = [&](int e) {
             return to_f32<T>(row[e]) + 0.0f == ll && (p.bias ? p.bias[e] : 0.f) == lb;

@@ -389,3 +389,26 @@ def test_sqrtsoftplus_far_below_zero(renorm):
     grad = want * slope * (up - (up * want / 2.5).sum(1, keepdim=True) if renorm else up)
     got = dl.double().gather(1, at)
     assert ((got - grad).abs() <= REL * want * (up.abs() + (3.75 if renorm else 0))).all()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "sqrtsoftplus", "softmax"])
+@pytest.mark.parametrize("groups,kept", [(1, 1), (8, 3), (32, 5)])
+def test_biases_of_the_lowest_value(groups, kept, score):
+    """The type's lowest value as a bias is a number: such experts come last, by their logits, but
+    before those that -inf masks, and a group of them before a group without any."""
+    E, k = 64, 8
+    lowest = torch.finfo(FL).min
+    l, bias = _logits(60, E, FL, 11)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    l[:40][torch.rand(40, E, generator=g, device="cuda") < 0.5] = -math.inf
+    l[20:30, :48] = -math.inf
+    l[30:34] = 0.5  # equal logits
+    for many in (4, 10, 58, 64):
+        b = bias.clone()
+        b[torch.randperm(E, generator=g, device="cuda")[:many]] = lowest
+        _check(_cfg(E, k, groups, kept, score), l, b)
+        b[:8] = -math.inf  # whole groups without an expert
+        _check(_cfg(E, k, groups, kept, score), l, b)
+    b = torch.full((E,), lowest, device="cuda")
+    b[3], b[40] = 0.5 * lowest, -lowest
+    _check(_cfg(E, k, groups, kept, score), l, b)
