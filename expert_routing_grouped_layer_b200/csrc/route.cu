@@ -584,6 +584,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwd p) {
                 }
             }
             m = warp_max(top);
+            if (m == -kInf) m = 0.f;  // every expert is masked: all scores are zero
             float zs = 0.f;
 #pragma unroll
             for (int j = 0; j < NI * VEC; ++j) {
@@ -591,8 +592,10 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteBwd p) {
                 zs += s[j];
             }
             z = warp_sum(zs);
+            if (z == 0.f) z = 1.f;
         } else {
             m = warp_max(valid ? l : -kInf);  // renormalised: a softmax over the chosen
+            if (m == -kInf) m = 0.f;
         }
     }
     const float w = chosen_weight(l, valid, p.score_fn, p.norm, m, z);

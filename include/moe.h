@@ -402,7 +402,8 @@ moe_status moe_route(const moe_config *cfg, int32_t dtype, const void *logits, i
  *  dl = G_j ds/dl at the chosen experts (sigmoid, sqrtsoftplus), or for the softmax
  *  dl_e = s_e (G_e - sum_j G_j p_j) at all experts (zero for those not chosen when
  *  norm_topk_prob). Slots with an index outside [0, E) take no part, whatever their
- *  dtopk_w; a row without a slot that does has a zero gradient. Every element of the
+ *  dtopk_w; a row without a slot that does has a zero gradient, and so has a masked
+ *  expert (logit -inf, s = 0) that a slot names. Every element of the
  *  T rows of dlogits is written. dlogits must not overlap logits. */
 moe_status moe_route_backward(const moe_config *cfg, int32_t dtype, const void *logits, int64_t ld,
                               int32_t T, const int32_t *topk_idx, const float *dtopk_w,

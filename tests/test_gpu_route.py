@@ -412,3 +412,28 @@ def test_biases_of_the_lowest_value(groups, kept, score):
     b = torch.full((E,), lowest, device="cuda")
     b[3], b[40] = 0.5 * lowest, -lowest
     _check(_cfg(E, k, groups, kept, score), l, b)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "sqrtsoftplus", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E", [64, 61])
+def test_backward_of_masked_experts_in_slots(E, renorm, score):
+    """Slots that name masked experts, some of a row's or all of them, in rows with and without others."""
+    l, _ = _logits(5, E, FL, 21)
+    l[0] = -math.inf
+    l[1, :4] = -math.inf
+    l[2, :2] = -math.inf
+    l[3, 1:] = -math.inf
+    idx = torch.arange(4, device="cuda", dtype=torch.int32).expand(5, 4).contiguous()
+    dw = torch.randn(5, 4, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    cfg = _cfg(E, 4, score=score, renorm=renorm)
+    dl = torch.full_like(l, 9)
+    moe.moe_route_backward(cfg, l, idx, dw, dl)
+    assert torch.isfinite(dl).all() and (dl[l == -math.inf] == 0).all()
+    assert (dl[1] == 0).all() if renorm or score != "softmax" else True
+    _check_backward(cfg, l[4:], idx[4:].contiguous(), dw[4:].contiguous())
+    # the row whose other slots are unmasked: as if those alone had been chosen
+    two = torch.full_like(dl[2:3], 9)
+    only = torch.tensor([[-1, -1, 2, 3]], dtype=torch.int32, device="cuda")
+    moe.moe_route_backward(cfg, l[2:3], only, dw[2:3].contiguous(), two)
+    assert ((dl[2:3] - two).abs() <= REL * two.abs() + REL * 2.5 * dw[2].abs().max()).all()
