@@ -328,7 +328,9 @@ def moe_layer_forward_prenorm(cfg, x, T, norm_w, eps, weights, out, ws, dev_stat
 # The operators below take tensors; the native module next to this file (csrc/binding.cpp)
 # reads sizes, strides and types from them, checks them (ValueError) and calls the library.
 # The tensors have to lie on one CUDA device, which is current during the call; without a
-# `stream` the call goes to that device's current stream.
+# `stream` the call goes to that device's current stream. No call records an autograd graph:
+# a tensor that requires a gradient is refused (ValueError) while gradients are enabled, as by
+# torch's out= forms; call under torch.no_grad() or inside an autograd.Function.
 BINDING_PATH = os.path.join(_HERE, "_binding.so")
 _BOUND = ("moe_norm", "moe_norm_backward", "moe_route", "moe_route_backward", "moe_combine_backward",
           "moe_linear", "moe_linear_backward")

@@ -7,7 +7,10 @@
 // The library's functions come by address (bind), so that one loaded libmoe.so serves both
 // this module and ctypes. Every function returns the library's status; wrong tensors raise
 // ValueError before the library is called. Type, shape and layout are checked before the
-// device.
+// device. No call records a graph, so a tensor that requires a gradient is refused where torch
+// would record one, as by torch's own out= forms, and the version counters of the outputs are
+// raised, by which torch's backward notices a saved tensor that was overwritten.
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -91,6 +94,11 @@ class Call {
         expect(name, t, type, {r, c});
         return layout(name, t);
     }
+    Rows out_rows(int i, const char* name, int64_t r, int64_t c, bool optional = false) {
+        const Rows o = rows(i, name, r, c, optional);
+        written(i);
+        return o;
+    }
     // A contiguous tensor of the given type and shape; None gives null.
     template <typename T = float>
     T* vec(int i, const char* name, c10::ScalarType st, c10::IntArrayRef shape) {
@@ -100,12 +108,19 @@ class Call {
         if (!t.is_contiguous()) throw Refused(std::string(name) + " must be contiguous");
         return static_cast<T*>(t.data_ptr());
     }
+    template <typename T = float>
+    T* out_vec(int i, const char* name, c10::ScalarType st, c10::IntArrayRef shape) {
+        T* p = vec<T>(i, name, st, shape);
+        written(i);
+        return p;
+    }
     void* bytes(int i, const char* name, size_t& n) {
         n = 0;
         if (a_[i] == Py_None) return nullptr;
         const at::Tensor& t = tensor(i, name);
         if (!t.is_contiguous()) throw Refused(std::string(name) + " must be contiguous");
         n = t.nbytes();
+        written(i);
         return t.data_ptr();
     }
     // Runs f(stream) with the operands' device current, without the interpreter lock.
@@ -119,6 +134,8 @@ class Call {
         Py_BEGIN_ALLOW_THREADS;
         status = f(stream);
         Py_END_ALLOW_THREADS;
+        if (status == MOE_OK)
+            for (int i = 0; i < n_written_; ++i) THPVariable_Unpack(a_[written_[i]]).unsafeGetTensorImpl()->bump_version();
         return PyLong_FromLong(status);
     }
     int dtype() const { return type == BF16 ? MOE_T_BF16 : type == F32 ? MOE_T_F32 : MOE_T_F16; }
@@ -137,6 +154,9 @@ class Call {
         if (!THPVariable_Check(o)) throw Refused(std::string(name) + " is not a tensor");
         const at::Tensor& t = THPVariable_Unpack(o);
         if (t.layout() != c10::kStrided) throw Refused(std::string(name) + " is not a strided tensor");
+        if (t.requires_grad() && at::GradMode::is_enabled())
+            throw Refused(std::string(name) + " requires a gradient, but no graph is recorded here: call under "
+                                              "torch.no_grad() or pass its detach()");
         if (!first_name_) {
             first_name_ = name;
             first_ = t.device();
@@ -160,7 +180,11 @@ class Call {
                           "; the elements of a row must be adjacent and rows must not overlap");
         return r;
     }
+    void written(int i) {
+        if (a_[i] != Py_None && !THPVariable_Unpack(a_[i]).is_inference()) written_[n_written_++] = i;
+    }
     PyObject* const* a_;
+    int written_[6], n_written_ = 0;  // arguments that the call writes
     const char* first_name_ = nullptr;
     c10::Device first_ = c10::Device(c10::kCPU);
 };
@@ -184,11 +208,11 @@ PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const double eps = PyFloat_AsDouble(args[3]);
         if (PyErr_Occurred()) throw Refused("eps is not a number");
         const Rows x = c.matrix(0, "x");
-        const Rows y = c.rows(4, "y", x.rows, x.cols);
+        const Rows y = c.out_rows(4, "y", x.rows, x.cols);
         const float* w = c.vec(1, "w", F32, {x.cols});
         const float* b = c.vec(2, "b", F32, {x.cols});
-        float* mean = c.vec(5, "mean", F32, {x.rows});
-        float* rstd = c.vec(6, "rstd", F32, {x.rows});
+        float* mean = c.out_vec(5, "mean", F32, {x.rows});
+        float* rstd = c.out_vec(6, "rstd", F32, {x.rows});
         const int kind = c.number(7);
         return c.run(8, [&](void* st) {
             return api.norm(kind, c.dtype(), x.p, x.ld, x.rows, x.cols, w, b, (float)eps, y.p, y.ld, mean, rstd, st);
@@ -202,12 +226,12 @@ PyObject* norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
         Call c(args, n, 11);
         const Rows x = c.matrix(1, "x");
         const Rows dy = c.rows(0, "dy", x.rows, x.cols);
-        const Rows dx = c.rows(5, "dx", x.rows, x.cols, true);
+        const Rows dx = c.out_rows(5, "dx", x.rows, x.cols, true);
         const float* w = c.vec(2, "w", F32, {x.cols});
         const float* mean = c.vec(3, "mean", F32, {x.rows});
         const float* rstd = c.vec(4, "rstd", F32, {x.rows});
-        float* dw = c.vec(6, "dw", F32, {x.cols});
-        float* db = c.vec(7, "db", F32, {x.cols});
+        float* dw = c.out_vec(6, "dw", F32, {x.cols});
+        float* db = c.out_vec(7, "db", F32, {x.cols});
         size_t nws;
         void* ws = c.bytes(8, "ws", nws);
         const int kind = c.number(9);
@@ -232,8 +256,8 @@ PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const moe_config* cfg = c.config(0);
         const Rows l = router(c, 1, cfg);
         const float* bias = c.vec(2, "bias", F32, {l.cols});
-        int32_t* idx = c.vec<int32_t>(3, "topk_idx", I32, {l.rows, cfg->num_experts_per_tok});
-        float* w = c.vec(4, "topk_w", F32, {l.rows, cfg->num_experts_per_tok});
+        int32_t* idx = c.out_vec<int32_t>(3, "topk_idx", I32, {l.rows, cfg->num_experts_per_tok});
+        float* w = c.out_vec(4, "topk_w", F32, {l.rows, cfg->num_experts_per_tok});
         return c.run(5, [&](void* st) { return api.route(cfg, c.dtype(), l.p, l.ld, l.rows, bias, idx, w, st); });
     });
 }
@@ -246,7 +270,7 @@ PyObject* route_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const Rows l = router(c, 1, cfg);
         const int32_t* idx = c.vec<int32_t>(2, "topk_idx", I32, {l.rows, cfg->num_experts_per_tok});
         const float* dw = c.vec(3, "dtopk_w", F32, {l.rows, cfg->num_experts_per_tok});
-        const Rows d = c.rows(4, "dlogits", l.rows, l.cols);
+        const Rows d = c.out_rows(4, "dlogits", l.rows, l.cols);
         return c.run(5, [&](void* st) {
             return api.route_backward(cfg, c.dtype(), l.p, l.ld, l.rows, idx, dw, d.p, d.ld, st);
         });
@@ -264,8 +288,8 @@ PyObject* combine_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const void* y = c.vec<void>(2, "y", BF16, {T * k, H});
         const int32_t* row_of = c.vec<int32_t>(3, "row_of", I32, {T * k});
         const float* w = c.vec(4, "topk_w", F32, {T, k});
-        void* dy = c.vec<void>(5, "dy", BF16, {T * k, H});
-        float* dw = c.vec(6, "dtopk_w", F32, {T, k});
+        void* dy = c.out_vec<void>(5, "dy", BF16, {T * k, H});
+        float* dw = c.out_vec(6, "dtopk_w", F32, {T, k});
         return c.run(7, [&](void* st) { return api.combine_backward(cfg, dout, y, row_of, w, (int32_t)T, dy, dw, st); });
     });
 }
@@ -279,11 +303,11 @@ PyObject* linear(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const int64_t N = c.matrix(1, "w").rows;
         c.type = t;
         const Rows w = c.rows(1, "w", N, x.cols);
-        const Rows y = c.rows(4, "y", x.rows, N);
+        const Rows y = c.out_rows(4, "y", x.rows, N);
         const float* bias = c.vec(2, "bias", F32, {N});
-        const Rows res = c.rows(3, "residual", x.rows, N, true), pre = c.rows(5, "pre", x.rows, N, true);
+        const Rows res = c.rows(3, "residual", x.rows, N, true), pre = c.out_rows(5, "pre", x.rows, N, true);
         const int act = c.number(6);
-        int32_t* status = c.vec<int32_t>(7, "dev_status", I32, {1});
+        int32_t* status = c.out_vec<int32_t>(7, "dev_status", I32, {1});
         return c.run(8, [&](void* st) {
             return api.linear(c.dtype(), x.p, x.ld, w.p, w.ld, bias, res.p, res.ld, act, x.rows, (int32_t)N, x.cols,
                               y.p, y.ld, pre.p, pre.ld, status, st);
@@ -301,13 +325,13 @@ PyObject* linear_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
         c.type = t;
         const Rows w = c.rows(2, "w", N, x.cols);
         const Rows dy = c.rows(0, "dy", x.rows, N);
-        const Rows pre = c.rows(3, "pre", x.rows, N, true), dx = c.rows(4, "dx", x.rows, x.cols, true),
-                   dw = c.rows(5, "dw", N, x.cols, true);
-        float* db = c.vec(6, "db", F32, {N});
+        const Rows pre = c.rows(3, "pre", x.rows, N, true), dx = c.out_rows(4, "dx", x.rows, x.cols, true),
+                   dw = c.out_rows(5, "dw", N, x.cols, true);
+        float* db = c.out_vec(6, "db", F32, {N});
         size_t nws;
         void* ws = c.bytes(7, "ws", nws);
         const int act = c.number(8);
-        int32_t* status = c.vec<int32_t>(9, "dev_status", I32, {1});
+        int32_t* status = c.out_vec<int32_t>(9, "dev_status", I32, {1});
         return c.run(10, [&](void* st) {
             return api.linear_backward(c.dtype(), dy.p, dy.ld, x.p, x.ld, w.p, w.ld, pre.p, pre.ld, act, x.rows,
                                        (int32_t)N, x.cols, dx.p, dx.ld, dw.p, dw.ld, db, ws, nws, status, st);

@@ -202,3 +202,34 @@ def test_missing_binding_fails_loudly(lib, monkeypatch, tmp_path):
     monkeypatch.setattr(moe, "_binding", None)
     with pytest.raises(RuntimeError, match="not built"):
         moe.moe_norm(torch.zeros(4, 64), None, None, 1e-6, torch.zeros(4, 64))
+
+
+def _seven():
+    """Every operator with small CPU tensors (refused at the latest for their device), as (call,
+    arguments that are tensors)."""
+    z = torch.zeros
+    cfg = W.CONFIGS["tiny_bf16"]
+    E, k, H = cfg.n_routed_experts, cfg.num_experts_per_tok, cfg.hidden
+    m = lambda *s: z(*s, dtype=BF)
+    return [(moe.moe_norm, (m(4, 64), z(64), z(64), 1e-6, m(4, 64), z(4), z(4))),
+            (moe.moe_norm_backward, (m(4, 64), m(4, 64), z(64), z(4), z(4), m(4, 64), z(64), z(64), z(64))),
+            (moe.moe_route, (cfg, z(4, E), z(E), z(4, k, dtype=I32), z(4, k))),
+            (moe.moe_route_backward, (cfg, z(4, E), z(4, k, dtype=I32), z(4, k), z(4, E))),
+            (moe.moe_combine_backward, (cfg, m(4, H), m(4 * k, H), z(4 * k, dtype=I32), z(4, k), m(4 * k, H), z(4, k))),
+            (moe.moe_linear, (m(4, 64), m(8, 64), z(8), m(4, 8), m(4, 8), m(4, 8))),
+            (moe.moe_linear_backward, (m(4, 8), m(4, 64), m(8, 64), m(4, 8), m(4, 64), m(8, 64), z(8), z(64)))]
+
+
+def test_binding_refuses_tensors_that_require_a_gradient(lib):
+    """No graph is recorded, so nothing that torch would record passes unnoticed."""
+    for fn, args in _seven():
+        for i, a in enumerate(args):
+            if not (isinstance(a, torch.Tensor) and a.is_floating_point()):
+                continue
+            given = list(args)
+            given[i] = a.clone().requires_grad_()
+            _refused("requires a gradient", fn, *given)
+            with torch.no_grad():
+                _refused("not on a CUDA device", fn, *given)
+            given[i] = given[i].detach()
+            _refused("not on a CUDA device", fn, *given)
