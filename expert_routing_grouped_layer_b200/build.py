@@ -20,6 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoe.so")
 BINDING = os.path.join(HERE, "_binding.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_STAMP = os.path.join(HERE, "_binding.torch")  # the torch version it was compiled for
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -47,15 +48,24 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def _binding_stale(torch_version: str) -> bool:
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_STAMP):
+        return True
+    with open(BINDING_STAMP) as f:
+        if f.read() != torch_version:
+            return True
+    t = os.path.getmtime(BINDING)
+    return any(os.path.getmtime(d) > t for d in (BINDING_SRC, os.path.join(INCLUDE, "moe.h")))
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """Compile the native module against the installed torch's headers (no nvcc)."""
-    deps = [BINDING_SRC, os.path.join(INCLUDE, "moe.h")]
-    if not force and os.path.exists(BINDING) and all(
-            os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
-        return BINDING
+    """Compile the native module against the installed torch's headers (no nvcc). It is
+    compiled again when its sources or torch's version change."""
     import sysconfig
 
     import torch
+    if not force and not _binding_stale(torch.__version__):
+        return BINDING
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     tmp = BINDING + ".tmp%d" % os.getpid()
@@ -69,11 +79,12 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(torch.__version__)
     return BINDING
 
 
-def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    build_binding(force, verbose)
+def build_library(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not _stale():
         return LIB
     tmp = LIB + ".tmp%d" % os.getpid()
@@ -82,6 +93,17 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    """The library, which needs no torch, then the native module, which is left out where
+    torch is not installed (the calls that need it say so)."""
+    build_library(force, verbose, extra)
+    try:
+        build_binding(force, verbose)
+    except ImportError as e:
+        print("%s is not built: %s" % (os.path.basename(BINDING), e), file=sys.stderr)
     return LIB
 
 
