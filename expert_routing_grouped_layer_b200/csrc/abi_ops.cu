@@ -15,11 +15,9 @@ static inline bool aligned(const void* p, size_t a) {
 
 static inline bool dtype_ok(int d) { return d == MOE_T_BF16 || d == MOE_T_F16 || d == MOE_T_F32; }
 
-static inline size_t dtype_size(int d) { return d == MOE_T_F32 ? 4 : 2; }
-
 // A row operand: present, aligned to its elements, rows that do not overlap.
 static inline bool rows_ok(const void* p, int64_t ld, int64_t cols, int dtype) {
-    return p && ld >= cols && ld <= (int64_t)1 << 40 && aligned(p, dtype_size(dtype));
+    return p && ld >= cols && ld <= (int64_t)1 << 40 && aligned(p, esize(dtype));
 }
 
 // A matrix that TMA reads: 16-byte aligned rows; the stride of a single row counts for

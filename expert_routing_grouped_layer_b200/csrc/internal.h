@@ -40,6 +40,7 @@ struct WsLayout {
 };
 
 bool config_valid(const moe_config* c);
+inline int esize(int dtype) { return dtype == MOE_T_F32 ? 4 : 2; }  // of a MOE_T_* element
 // Raises a kernel's opt-in dynamic shared-memory limit on the current device to
 // at least `bytes`; the size set per (kernel, device) pair is cached, so a call
 // at or below it does nothing. A failed call leaves the cached size as it was.

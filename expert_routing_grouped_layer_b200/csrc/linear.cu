@@ -23,7 +23,7 @@
 //                        partial tiles through distributed shared memory in rank order,
 //                        so the weights stream through all SMs and equal calls give
 //                        equal bits. Bound by the weights' bytes and ~4 us of launch, set-up
-//                        and exchange: one token, 2048 x 7168, 8.2-8.6 us.
+//                        and exchange: one token, 2048 x 7168, 8.5-8.7 us.
 // Sums are fp32 in tensor memory; y, pre, dx and dW are rounded once to the tensors'
 // type, and g once between dy and the products (the tensor cores take 16-bit operands).
 #include <type_traits>
@@ -921,7 +921,7 @@ __device__ __forceinline__ Pack<T, VEC> act_grad(const Pack<T, VEC>& a, const Pa
 }
 
 // CTA (x, y): 32 VEC columns x `rows` rows; warp w takes rows w, w + 8, ..., four at a time
-// so that eight loads are in flight (one row at a time: 91 us instead of 70 for 8192 x 7168 SiLU).
+// so that eight loads are in flight (one row at a time: 91 us, four: 70; 8192 x 7168 SiLU).
 // The column sums of the unrounded products stay in registers, then cross the warps once.
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(256) linear_act_bwd_kernel(ActBwd p) {
@@ -1043,7 +1043,9 @@ struct Plan {
 
 // CTAs of `split`-CTA clusters that fit on the device at once, `per_sm` to an SM. Clusters of
 // 4 and 8 leave SMs over (a GPC's SMs do not divide evenly): on a 148-SM B200 the driver
-// reports 148, 148, 132, 120 CTAs one to an SM, and 296, 296, 284, 264 two to an SM.
+// reports 148, 148, 132, 120 CTAs one to an SM, and 296, 296, 284, 264 two to an SM. Constants,
+// not a query: how the SMs of one GPU are spread over its GPCs must not decide the split, and with
+// it the order of the additions.
 int cluster_capacity(int split, int per_sm) {
     static const float share[2][4] = {{1.0f, 1.0f, 132.f / 148, 120.f / 148}, {1.0f, 1.0f, 284.f / 296, 264.f / 296}};
     const int l = split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3;

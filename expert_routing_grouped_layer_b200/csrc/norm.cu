@@ -12,12 +12,12 @@
 // store, so the mean, the centred squares (two reductions, no cancellation) and the
 // output come from one read. Kernels, by the rows' shape:
 //   norm_fwd_kernel         fewer rows than 2 per SM: a row per CTA, straight from registers
-//                           (128 x 7168: 3.0 us);
+//                           (128 x 7168: 2.9 us);
 //   norm_*_ring_kernel      many rows on the 16-byte grid: persistent CTAs behind a ring of
 //                           rows in shared memory (16384 x 7168 bf16 forward 79 us, 0.90 of
 //                           measured HBM; 8192 x 7168 backward 65 us, 0.83, of which 5 us
 //                           are the column sums' second kernel);
-//   norm_*_ragged_kernel    rows off the grid (8192 x 7166: forward 80 us, backward 150 us;
+//   norm_*_ragged_kernel    rows off the grid (8192 x 7166: forward 82 us, backward 151 us;
 //                           bound by their instructions).
 // The arithmetic runs two elements to an instruction (packed fp32): with single operations
 // the forward pass was bound by instruction issue (102 us).
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_ring_kernel(NormFwd p) {
     }
 }
 
-// Sums over the CTA of N values (4 or 8), the same bits in every thread. Within a warp the
+// Sums over the CTA of N values (2 or 4), the same bits in every thread. Within a warp the
 // values share the butterfly: log2 N exchanges leave each lane one value's partial sum
 // (value lane % N). Then every warp adds the warps' sums, 32 / N lanes per value.
 template <int N>
@@ -921,10 +921,6 @@ cudaError_t bwd_type(int layer, const NormBwd& p, bool vec, float* dw, float* db
     constexpr int S = sizeof(T) == 2 ? 3 : 1;
     if (p.T < 4 * num_sms()) return bwd_ring<T, NV, 1, 2 * S, 512>(layer, p, dw, db, st);
     return bwd_ring<T, NV, 2, S, 512>(layer, p, dw, db, st);
-}
-
-inline bool rows16(const void* p, long ld, int es) {
-    return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * es) % 16 == 0);
 }
 
 }  // namespace

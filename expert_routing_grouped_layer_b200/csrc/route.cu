@@ -664,10 +664,6 @@ void fwd_type(const RouteParams& p, bool vec, cudaStream_t st) {
     else fwd<T, 1, 64>(p, L, st);
 }
 
-inline bool rows16(const void* p, long ld, int es) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * es) % 16 == 0;
-}
-
 }  // namespace
 
 cudaError_t launch_route(const moe_config* c, int dtype, const void* logits, long ld, int T,

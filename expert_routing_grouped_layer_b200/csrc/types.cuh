@@ -10,8 +10,7 @@
 namespace moe {
 
 // exp(x) and 1 / x by one special-function operation each, subnormal results as zero: within
-// 2^-22 + |x| 2^-23 and 2^-23 of the value. (The intrinsics' handling of subnormals costs
-// three more instructions.)
+// 2^-22 + |x| 2^-23 and 2^-23 of the value.
 __device__ __forceinline__ float exp_approx(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
@@ -158,6 +157,9 @@ __device__ __forceinline__ uint4 narrow8(const float* v) {
     return make_uint4(x.x, x.y, y.x, y.y);
 }
 
-inline int esize(int dtype) { return dtype == MOE_T_F32 ? 4 : 2; }
+// Rows of es-byte elements that 16-byte accesses reach; true for a matrix that is not there.
+inline bool rows16(const void* p, long ld, int es) {
+    return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * es) % 16 == 0);
+}
 
 }  // namespace moe

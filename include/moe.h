@@ -353,8 +353,10 @@ moe_status moe_layer_forward_prenorm(const moe_config *cfg, const void *x, int32
  *  NULL; mean is not written for MOE_NORM_RMS. eps finite, >= 0. 1 <= H <= 16384,
  *  larger rows return MOE_ERR_UNSUPPORTED. Statistics and arithmetic are fp32, y is
  *  rounded once; a row of finite values whose (centred) squares add up to more than
- *  fp32 holds has rstd = 0 and so y = b. Rows whose base, stride and length are multiples of 16 bytes move
- *  by 16-byte accesses; others element by element. */
+ *  fp32 holds has rstd = 0 and so y = b. Rows move by 16-byte accesses. Where a base, stride
+ *  or length is not a multiple of 16 bytes, the aligned 16 bytes around a row's ends are read
+ *  as well (inside the matrix only: its other rows and what lies between them; the values
+ *  are not used); of an output only the rows' own elements are written. */
 moe_status moe_norm(int32_t kind, int32_t dtype, const void *x, int64_t ldx, int32_t T, int32_t H,
                     const float *w, const float *b, float eps, void *y, int64_t ldy, float *mean,
                     float *rstd, void *stream);
@@ -429,7 +431,8 @@ moe_status moe_combine_backward(const moe_config *cfg, const void *dout, const v
  *  the backward pass) or is NULL; these three may have any stride >= N and any alignment
  *  of their elements. y may be residual when the strides are equal; no other output may
  *  overlap an input. act MOE_ACT_*. Products accumulate in fp32 (a NaN or infinity in x
- *  or w reaches the rows and columns it belongs to); y is rounded once. The order of the
+ *  or w reaches the rows and columns it belongs to); act(z) is right to 2^-14 of its own
+ *  value, tails included, and y is rounded once. The order of the
  *  additions depends on the sizes and the GPU alone. MOE_DEV_TIMEOUT in *dev_status (may
  *  be NULL) if a pipeline wait ran out. M = 0 does nothing; N, K >= 1. */
 moe_status moe_linear(int32_t dtype, const void *x, int64_t ldx, const void *w, int64_t ldw,
@@ -443,7 +446,8 @@ moe_status moe_linear(int32_t dtype, const void *x, int64_t ldx, const void *w, 
  *  dy, pre [M][N] of `dtype`: pre as moe_linear wrote it, NULL allowed for MOE_ACT_NONE.
  *  x and w as in moe_linear; dy, pre, dx, dw may have any stride >= their width and any
  *  alignment of their elements. g is rounded to `dtype` between the elementwise step and
- *  the products (not in db); dx and dw are rounded once and overwritten; M = 0 sets dw
+ *  the products, which take 16-bit operands (not in db: dx and dw of bf16 are off by 2.4e-3 of
+ *  their norm, 1.7e-3 of it their own rounding); dx and dw are rounded once and overwritten; M = 0 sets dw
  *  and db to zero. Outputs must not overlap inputs. ws: 16-byte aligned,
  *  moe_linear_backward_workspace_bytes bytes. */
 moe_status moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void *x,
