@@ -85,8 +85,10 @@ __device__ __forceinline__ void with_score(int fn, F&& f) {
 // e^l leaves the type's range while e^(l/2) is an ordinary number (from l = -88 on in fp32).
 __device__ __forceinline__ float score_f(float l, int fn, float m, float inv_z) {
     if (fn == MOE_SCORE_SIGMOID) return 1.0f / (1.0f + expf(-l));
-    if (fn == MOE_SCORE_SQRTSOFTPLUS)  // at -20 the other terms are 5e-10 of it
-        return l < -20.0f ? expf(0.5f * l) : sqrtf(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
+    if (fn == MOE_SCORE_SQRTSOFTPLUS) {
+        const float e = expf(-0.5f * fabsf(l));
+        return l < -20.0f ? e : sqrtf(fmaxf(l, 0.0f) + log1pf(e * e));  // at -20 the rest is 5e-10 of e
+    }
     return expf(l - m) * inv_z;
 }
 __device__ __forceinline__ double score_d(double l, int fn, double m, double z) {
