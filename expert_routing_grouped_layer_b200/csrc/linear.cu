@@ -16,8 +16,9 @@
 //   linear_pair_kernel   many rows: persistent CTA pairs (cta_group::2), a 256 x BN tile
 //                        per pair, accumulators double-buffered in tensor memory. Bound by
 //                        the tensor cores and the power cap: 8192 x 7168 x 2048 with bias
-//                        and residual in 168-175 us (1.43 PFLOP/s, tensor pipe 90% active at
-//                        1.5 GHz); a library product of that size alone took 168-200;
+//                        and residual in 166-180 us (1.34-1.45 PFLOP/s, tensor pipe 91% active at
+//                        1.5 GHz; 193-205 us in a long run); a library product of that size
+//                        alone took 168-172;
 //   linear_split_kernel  few tiles (serving, small gradients): 128 columns x BT rows per
 //                        cluster of up to 8 CTAs that share the k range and add their
 //                        partial tiles through distributed shared memory in rank order,

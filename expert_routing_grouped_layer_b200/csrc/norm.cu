@@ -17,7 +17,7 @@
 //                           rows in shared memory (16384 x 7168 bf16 forward 79 us, 0.90 of
 //                           measured HBM; 8192 x 7168 backward 65 us, 0.83, of which 5 us
 //                           are the column sums' second kernel);
-//   norm_*_ragged_kernel    rows off the grid (8192 x 7166: forward 82 us, backward 151 us;
+//   norm_*_ragged_kernel    rows off the grid (8192 x 7166: forward 81 us, backward 150 us;
 //                           bound by their instructions).
 // The arithmetic runs two elements to an instruction (packed fp32): with single operations
 // the forward pass was bound by instruction issue (102 us).
