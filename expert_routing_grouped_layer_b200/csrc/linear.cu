@@ -252,6 +252,18 @@ __device__ __forceinline__ void store4(const Epilogue& e, float4 acc, float4 b, 
     }
 }
 
+// The first n elements of a lane's row of a 32 x 32 block of 16-bit elements in swizzled shared
+// memory (16-byte piece j at j ^ swz) to a row in memory that starts on a 16-byte boundary.
+__device__ __forceinline__ void copy_row_part(void* out, const uint8_t* row, int swz, int n) {
+    int j = 0;
+#pragma unroll 1
+    for (; 8 * j + 8 <= n; ++j)
+        static_cast<uint4*>(out)[j] = *reinterpret_cast<const uint4*>(row + ((j ^ swz) << 4));
+#pragma unroll 1
+    for (int i = 8 * j; i < n; ++i)
+        static_cast<uint16_t*>(out)[i] = *reinterpret_cast<const uint16_t*>(row + ((j ^ swz) << 4) + 2 * (i & 7));
+}
+
 struct GemmDims {
     int R, C, K;  // out rows, out columns, reduction length
     int32_t* status;
@@ -264,7 +276,9 @@ struct GemmDims {
 //   groups that take alternate 32-column chunks.
 // Epilogue with outputs on the 16-byte grid (TMA_OUT): a lane finishes one row's 32 columns
 // in registers, the warp's 32 x 32 block goes through 2 KB of swizzled shared memory and
-// leaves (and the residual comes) by TMA, which also clips it to the matrix. Otherwise a
+// leaves (and the residual comes) by TMA, which also clips it to the matrix. It clips in
+// steps of 16 bytes: a row's last chunk, where the width is not a multiple of 8, is stored
+// by the lanes, or the TMA would write up to 7 elements behind the row. Otherwise a
 // chunk goes through shared memory as fp32 and lanes store along rows, element by element
 // where need be; with the residual that took 13.8 us a tile against the main loop's 14.5 us
 // at K = 2048 and held the tensor cores up.
@@ -534,13 +548,18 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                     __syncwarp();
                     uint8_t* mine = buf + lane * 64;
                     const int swz = (lane >> 1) & 3;
+                    const bool clip = col + 32 > d.C && (d.C & 7) != 0;
                     if (has_pre) {
+                        uint8_t* mine_pre = bufs + 4096 + lane * 64;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<uint4*>(bufs + 4096 + lane * 64 + ((j ^ swz) << 4)) = narrow8<T>(&z[8 * j]);
+                            *reinterpret_cast<uint4*>(mine_pre + ((j ^ swz) << 4)) = narrow8<T>(&z[8 * j]);
+                        if (clip && row + lane < d.R)
+                            copy_row_part(static_cast<T*>(epi.pre) + (row + lane) * epi.ld_pre + col, mine_pre, swz,
+                                          d.C - col);
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0 && row < d.R) tma_store_2d(&tmO.pre, bufs + 4096, col, row);
+                        if (lane == 0 && row < d.R && !clip) tma_store_2d(&tmO.pre, bufs + 4096, col, row);
                     }
                     with_act(epi.act, [&](auto act) {
 #pragma unroll
@@ -567,10 +586,12 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         *reinterpret_cast<uint4*>(mine + ((j ^ swz) << 4)) = narrow8<T>(&z[8 * j]);
+                    if (clip && row + lane < d.R)
+                        copy_row_part(static_cast<T*>(epi.out) + (row + lane) * epi.ld_out + col, mine, swz, d.C - col);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        if (row < d.R) tma_store_2d(&tmO.out, buf, col, row);
+                        if (row < d.R && !clip) tma_store_2d(&tmO.out, buf, col, row);
                         bulk_commit();
                     }
                 }

@@ -321,3 +321,47 @@ def test_gradient_at_infinite_and_huge_pre(act, dt):
     want = torch.tensor([2.0] * 4 + [0.0] * 4, device="cuda")
     assert torch.equal(db[:8], want) and torch.isnan(db[8])
     assert torch.equal(g[:8, 0].float(), want) and torch.isnan(g[8, 0])
+
+
+def _between(rows, cols, extra, dt):
+    """A matrix inside a wider one of sevens, rows a multiple of 16 bytes apart; the wider one."""
+    wide = torch.full((rows, (cols + 7) // 8 * 8 + extra), 7.0, dtype=dt, device="cuda")
+    return wide[:, :cols], wide
+
+
+@pytest.mark.parametrize("extra", [0, 8, 40])
+@pytest.mark.parametrize("M,N,K", [(4, 23, 5), (17, 2791, 79), (149, 15, 4), (666, 7, 155), (3000, 1500, 64),
+                                   (2500, 1503, 65), (2500, 1505, 130), (1037, 2051, 1111), (300, 4097, 33)])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_what_lies_behind_ragged_rows_stays(M, N, K, extra, dt):
+    """Outputs whose rows start on 16-byte boundaries and end inside one: y, pre, dx and dw leave the
+    elements behind their rows as they are, and are right up to the last one."""
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    x, w = _mat(g, M, K, dt), _mat(g, N, K, dt, scale=K ** -0.5)
+    b = torch.randn(N, generator=g, device="cuda")
+    for res in (None, _mat(g, M, N, dt), "y"):
+        for with_pre in (False, True):
+            (y, wide), (z, zwide) = _between(M, N, extra, dt), _between(M, N, extra, dt)
+            r = res
+            if res == "y":  # in place
+                y.copy_(_mat(g, M, N, dt))
+                r = y.clone()
+            moe.moe_linear(x, w, b, y if res == "y" else res, y, z if with_pre else None, act="silu")
+            zd, yd = ref.linear(x, w, b, r, "silu")
+            err = acc_unit(K) * (x.double().abs() @ w.double().abs().t() + b.double().abs())
+            ev = 1.13 * err + 2.0 ** -21 * (1 + zd.abs()) + 2.0 ** -23 * (r.double().abs() if r is not None else 0)
+            assert ((y.double() - yd).abs() <= ref.U[dt] * yd.abs() + 1.01 * ev + TINY[dt]).all()
+            assert (wide[:, N:] == 7).all()
+            if with_pre:
+                assert ((z.double() - zd).abs() <= ref.U[dt] * zd.abs() + err * 1.01 + TINY[dt]).all()
+            assert (zwide[:, N:] == 7).all()
+    dy = _mat(g, M, N, dt)
+    (dx, xwide), (dw, wwide) = _between(M, K, extra, dt), _between(N, K, extra, dt)
+    ws = torch.empty(moe.moe_linear_backward_workspace_bytes(M, N, K), dtype=torch.uint8, device="cuda")
+    moe.moe_linear_backward(dy, x, w, None, dx, dw, None, ws)
+    assert (xwide[:, K:] == 7).all() and (wwide[:, K:] == 7).all()
+    gd, rdx, rdw, _ = ref.linear_backward(dy, x, w, None, "none")
+    tol = acc_unit(N) * 1.01 * (gd.abs() @ w.double().abs()) + ref.U[dt] * rdx.abs() * 1.01 + TINY[dt]
+    assert ((dx.double() - rdx).abs() <= tol).all()
+    tol = acc_unit(M) * 1.01 * (gd.abs().t() @ x.double().abs()) + ref.U[dt] * rdw.abs() * 1.01 + TINY[dt]
+    assert ((dw.double() - rdw).abs() <= tol).all()
