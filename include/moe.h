@@ -440,7 +440,7 @@ moe_status moe_linear(int32_t dtype, const void *x, int64_t ldx, const void *w, 
                       int32_t N, int32_t K, void *y, int64_t ldy, void *pre, int64_t ldp,
                       int32_t *dev_status, void *stream);
 
-/* Gradients of moe_linear: with g = dy * act'(pre),
+/* Gradients of moe_linear: with g = dy * act'(pre) (RELU: 0 where pre is 0),
  *  dx = g W  [M][K],  dw = g^T x  [N][K],  db = sum_m g  (fp32 [N]);
  *  the residual's gradient is dy itself. dx, dw, db may each be NULL (not wanted).
  *  dy, pre [M][N] of `dtype`: pre as moe_linear wrote it, NULL allowed for MOE_ACT_NONE.
