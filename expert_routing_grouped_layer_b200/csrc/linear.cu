@@ -252,16 +252,14 @@ __device__ __forceinline__ void store4(const Epilogue& e, float4 acc, float4 b, 
     }
 }
 
-// The first n elements of a lane's row of a 32 x 32 block of 16-bit elements in swizzled shared
-// memory (16-byte piece j at j ^ swz) to a row in memory that starts on a 16-byte boundary.
-__device__ __forceinline__ void copy_row_part(void* out, const uint8_t* row, int swz, int n) {
-    int j = 0;
-#pragma unroll 1
-    for (; 8 * j + 8 <= n; ++j)
-        static_cast<uint4*>(out)[j] = *reinterpret_cast<const uint4*>(row + ((j ^ swz) << 4));
-#pragma unroll 1
-    for (int i = 8 * j; i < n; ++i)
-        static_cast<uint16_t*>(out)[i] = *reinterpret_cast<const uint16_t*>(row + ((j ^ swz) << 4) + 2 * (i & 7));
+// The first n (1 to 7) of eight 16-bit elements to a 16-byte aligned place.
+__device__ __forceinline__ void store_rest(void* out, const void* piece, int n) {
+    const uint4 v = *static_cast<const uint4*>(piece);
+    char* o = static_cast<char*>(out);
+    if (n & 4) *reinterpret_cast<uint2*>(o) = make_uint2(v.x, v.y);
+    const uint32_t a = n & 4 ? v.z : v.x, b = n & 4 ? v.w : v.y;
+    if (n & 2) *reinterpret_cast<uint32_t*>(o + 2 * (n & 4)) = a;
+    if (n & 1) *reinterpret_cast<uint16_t*>(o + 2 * (n & 6)) = (uint16_t)(n & 2 ? b : a);
 }
 
 struct GemmDims {
@@ -276,9 +274,9 @@ struct GemmDims {
 //   groups that take alternate 32-column chunks.
 // Epilogue with outputs on the 16-byte grid (TMA_OUT): a lane finishes one row's 32 columns
 // in registers, the warp's 32 x 32 block goes through 2 KB of swizzled shared memory and
-// leaves (and the residual comes) by TMA, which also clips it to the matrix. It clips in
-// steps of 16 bytes: a row's last chunk, where the width is not a multiple of 8, is stored
-// by the lanes, or the TMA would write up to 7 elements behind the row. Otherwise a
+// leaves (and the residual comes) by TMA, which also clips it to the matrix. A store clips in
+// steps of 16 bytes and would write up to 7 elements behind rows of other widths: the tensor
+// maps of out and pre end at the last multiple of 8 columns, and the lanes store the rest. Otherwise a
 // chunk goes through shared memory as fp32 and lanes store along rows, element by element
 // where need be; with the residual that took 13.8 us a tile against the main loop's 14.5 us
 // at K = 2048 and held the tensor cores up.
@@ -548,18 +546,20 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
                     __syncwarp();
                     uint8_t* mine = buf + lane * 64;
                     const int swz = (lane >> 1) & 3;
-                    const bool clip = col + 32 > d.C && (d.C & 7) != 0;
+                    const int rest = d.C & 7, edge = d.C - rest;  // columns that the lanes store, from edge on
+                    const bool tail = rest != 0 && edge >= col && edge < col + 32 && row + lane < d.R;
+                    const int tail_at = (((edge - col) >> 3) ^ swz) << 4;
+                    const bool tma = lane == 0 && row < d.R && col < edge;
                     if (has_pre) {
                         uint8_t* mine_pre = bufs + 4096 + lane * 64;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             *reinterpret_cast<uint4*>(mine_pre + ((j ^ swz) << 4)) = narrow8<T>(&z[8 * j]);
-                        if (clip && row + lane < d.R)
-                            copy_row_part(static_cast<T*>(epi.pre) + (row + lane) * epi.ld_pre + col, mine_pre, swz,
-                                          d.C - col);
+                        if (tail)
+                            store_rest(static_cast<T*>(epi.pre) + (row + lane) * epi.ld_pre + edge, mine_pre + tail_at, rest);
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0 && row < d.R && !clip) tma_store_2d(&tmO.pre, bufs + 4096, col, row);
+                        if (tma) tma_store_2d(&tmO.pre, bufs + 4096, col, row);
                     }
                     with_act(epi.act, [&](auto act) {
 #pragma unroll
@@ -586,12 +586,12 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         *reinterpret_cast<uint4*>(mine + ((j ^ swz) << 4)) = narrow8<T>(&z[8 * j]);
-                    if (clip && row + lane < d.R)
-                        copy_row_part(static_cast<T*>(epi.out) + (row + lane) * epi.ld_out + col, mine, swz, d.C - col);
+                    if (tail)
+                        store_rest(static_cast<T*>(epi.out) + (row + lane) * epi.ld_out + edge, mine + tail_at, rest);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        if (row < d.R && !clip) tma_store_2d(&tmO.out, buf, col, row);
+                        if (tma) tma_store_2d(&tmO.out, buf, col, row);
                         bulk_commit();
                     }
                 }
@@ -1050,8 +1050,8 @@ inline bool on_grid(const void* p, long ld) {
     return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0);
 }
 template <typename T>
-bool out_map(CUtensorMap* tm, const void* p, long ld, const GemmDims& d) {
-    return make_tmap_2d(tm, kMapType<T>, p, d.R, d.C, ld * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+bool out_map(CUtensorMap* tm, const void* p, long ld, int rows, int cols) {
+    return make_tmap_2d(tm, kMapType<T>, p, rows, cols, ld * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // Which kernel and tile: the one whose busiest SM is done first, in SM cycles. A k block
@@ -1124,12 +1124,14 @@ cudaError_t product(const void* rp, long ldr, const void* cp, long ldc, const Ge
     const Plan p = plan_gemm<R_MN>(d.R, d.C, d.K);
     CUtensorMap tr, tc;
     if (p.pair) {
-        const bool tma_out = on_grid(e.out, e.ld_out) && on_grid(e.pre, e.ld_pre) && on_grid(e.res, e.ld_res);
+        // stores clip in steps of 16 bytes: their maps end at the last multiple of 8 columns
+        const int whole = d.C & ~7;
+        const bool tma_out = whole > 0 && on_grid(e.out, e.ld_out) && on_grid(e.pre, e.ld_pre) && on_grid(e.res, e.ld_res);
         OutMaps to;
         if (tma_out) {
-            if (!out_map<T>(&to.out, e.out, e.ld_out, d) ||
-                !out_map<T>(&to.pre, e.pre ? e.pre : e.out, e.pre ? e.ld_pre : e.ld_out, d) ||
-                !out_map<T>(&to.res, e.res ? e.res : e.out, e.res ? e.ld_res : e.ld_out, d))
+            if (!out_map<T>(&to.out, e.out, e.ld_out, d.R, whole) ||
+                !out_map<T>(&to.pre, e.pre ? e.pre : e.out, e.pre ? e.ld_pre : e.ld_out, d.R, whole) ||
+                !out_map<T>(&to.res, e.res ? e.res : e.out, e.res ? e.ld_res : e.ld_out, d.R, d.C))
                 return cudaErrorInvalidValue;
         }
         auto kernel = tma_out ? linear_pair_kernel<T, R_MN, C_MN, true> : linear_pair_kernel<T, R_MN, C_MN, false>;
