@@ -17,7 +17,7 @@
 //                        per pair, accumulators double-buffered in tensor memory. Bound by
 //                        the tensor cores and the power cap: 8192 x 7168 x 2048 with bias
 //                        and residual in 166-180 us (1.34-1.45 PFLOP/s, tensor pipe 91% active at
-//                        1.5 GHz; 193-205 us in a long run); a library product of that size
+//                        1.5 GHz; 193-211 us in a long run); a library product of that size
 //                        alone took 168-172;
 //   linear_split_kernel  few tiles (serving, small gradients): 128 columns x BT rows per
 //                        cluster of up to 8 CTAs that share the k range and add their
